@@ -19,7 +19,7 @@ import torch
 own = False
 
 BLOCK = 64
-E_MIN = -118                       # least scale exponent of the 8-bit cache
+E_MIN, E_MAX = -118, 120           # scale exponents of the 8-bit cache
 COARSE = 0.05                      # coarse scale of every case: a head selects its topic's blocks
 
 
@@ -94,20 +94,25 @@ def _lens(case):
 # ---------------------------------------------------------------- 8-bit values
 
 def _quantise(x):
-    """Codes (e4m3) and biased scale exponents of rows x [..., d]."""
+    """Codes (e4m3) and biased scale exponents of rows x [..., d]; a row with a NaN or an
+    infinity gets the scale byte 255, which stands for NaN."""
     x = x.float()
+    bad = ~torch.isfinite(x).all(-1)
     amax = torch.where(torch.isfinite(x), x.abs(), torch.zeros_like(x)).amax(-1)
     m, k = torch.frexp(amax)
     e = torch.where(m <= 0.875, k - 9, k - 8).clamp(min=E_MIN)
     e = torch.where(amax > 0, e, torch.full_like(e, E_MIN))
     y = x * torch.exp2(-e.float()).unsqueeze(-1)
-    y = torch.where(torch.isfinite(x), y, torch.full_like(y, math.nan))
-    return y.to(torch.float8_e4m3fn), (e + 127).to(torch.uint8)
+    y = torch.where(torch.isfinite(x), y, torch.zeros_like(y))
+    top = torch.where(e == E_MAX, torch.full_like(amax, 240.0), torch.full_like(amax, 448.0)).unsqueeze(-1)
+    y = torch.minimum(torch.maximum(y, -top), top)       # 256 2^120 would be no bf16 number
+    return y.to(torch.float8_e4m3fn), torch.where(bad, torch.full_like(e, 255), e + 127).to(torch.uint8)
 
 
 def _values(code, scale):
     """fp32 values that codes [..., d] with scale exponents [...] stand for."""
-    return code.float() * torch.exp2(scale.float() - 127.0).unsqueeze(-1)
+    f = torch.where(scale == 255, torch.full_like(scale, math.nan, dtype=torch.float32), torch.exp2(scale.float() - 127.0))
+    return code.float() * f.unsqueeze(-1)
 
 
 # ---------------------------------------------------------------- inputs
@@ -397,9 +402,10 @@ def _exact_values(x):
     e = torch.ceil(torch.log2(mag.clamp(min=2.0 ** -140) / 448.0))
     e = torch.where(mag > 448.0 * torch.exp2(e), e + 1, e)
     e = torch.where(mag <= 448.0 * torch.exp2(e - 1), e - 1, e).clamp(min=E_MIN)
-    y = x * torch.exp2(-e)
+    y = (x * torch.exp2(-e)).clamp(-448.0, 448.0)
+    y = torch.where(e == E_MAX, y.clamp(-240.0, 240.0), y)
     step = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
-    return torch.round(y / step) * step * torch.exp2(e)
+    return torch.where(torch.isfinite(x).all(-1, keepdim=True), torch.round(y / step) * step * torch.exp2(e), math.nan)
 
 
 def _exact_threshold(x, alpha):
