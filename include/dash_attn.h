@@ -383,6 +383,102 @@ DASH_API int dash_decode_noalloc(const void* q, const void* k_cache, const void*
  * DASH_ERR_NO_CONVERGE (as dash_get_device_status), or DASH_ERR_CUDA. */
 DASH_API int dash_decode_noalloc_status(dash_stream_t stream);
 
+/*
+ * 8-bit KV cache.  A cached row (the d keys or values of one token and KV head) is d e4m3 codes
+ * and one scale byte s; its elements stand for code * 2^(s - 127).
+ *   k_cache, v_cache  device bytes [B, Hkv, Tmax, d], 16-byte aligned
+ *   k_scale, v_scale  device bytes [B, Hkv, Tmax],    16-byte aligned
+ * Tmax must be a multiple of `block` and B * Hkv * Tmax below 2^31 (DASH_ERR_SHAPE).  For a row
+ * whose largest finite magnitude is amax, s - 127 is the least exponent e >= -118 with
+ * amax <= 448 * 2^e, and each code is its element * 2^-e rounded to the nearest e4m3 number, ties
+ * to even (448 is e4m3's largest: nothing saturates, but for magnitudes above 240 * 2^120, which
+ * are held as that, so that every held value is a bf16 number).  A row with a NaN or an infinity gets
+ * s = 255 and stands for NaN in every element.
+ */
+
+/*
+ * Appends rows to the 8-bit cache: token i < n_new[b] of sequence b goes to position kv_len[b] + i.
+ *   k_new, v_new  device bf16 [B, Hkv, n_rows, d]
+ *   src       device int32 [B, n] or NULL: token i is row src[b, i] of k_new and v_new (the
+ *             accepted path of a drafted tree); NULL: row i (n <= n_rows)
+ *   n_new     device int32 [B] or NULL: tokens appended per sequence, 0 <= n_new[b] <= n; NULL: n
+ *   kv_len    device int32 [B]: tokens held before the call (the caller advances it afterwards)
+ *   ksum      device fp32 [B, Hkv, Tmax / block, d] or NULL: the summary of every block that the
+ *             call completes, the mean of the block's held keys; other entries are left alone
+ * A sequence with kv_len[b] < 0, n_new[b] outside [0, n], kv_len[b] + n_new[b] > Tmax or a src
+ * entry below n_new[b] outside [0, n_rows) is left as it was.  The summaries depend on what the
+ * cache holds alone, so a caller may lower kv_len and append again over rejected tokens.
+ */
+DASH_API int dash_cache_append(const void* k_new, const void* v_new, const int* src, const int* n_new,
+                               const int* kv_len, void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                               float* ksum, int B, int Hkv, int n_rows, int n, int Tmax, int d, int block,
+                               dash_stream_t stream);
+
+/*
+ * Rows of the 8-bit cache as bf16 (exact): k_out, v_out [B, Hkv, n, d], row i of sequence b from
+ * position start[b] + i.
+ *   start   device int32 [B] or NULL (0)
+ *   kv_len  device int32 [B] or NULL (Tmax): rows whose position is negative, >= kv_len[b] or
+ *           >= Tmax are zero
+ */
+DASH_API int dash_cache_read(const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                             const int* start, const int* kv_len, void* k_out, void* v_out, int B, int Hkv, int n,
+                             int Tmax, int d, int block, dash_stream_t stream);
+
+/* Bytes of workspace dash_decode_q8 needs (0 when the shape is unsupported). */
+DASH_API size_t dash_decode_q8_workspace_size(int B, int Hq, int Hkv, int Tmax, int d, int block);
+
+/*
+ * dash_decode over the 8-bit cache: the result is that of dash_decode on the values that the
+ * cache holds, to fp32 rounding of the sums (fewer roundings inside: the weights of the values
+ * have 11 significant bits, where dash_decode's have 8).
+ *   ksum   as in dash_decode, of the held keys (dash_cache_append keeps it)
+ * At most 32 query heads per KV head.  More than 8 are worked on as equal parts of at most 8, each with
+ * the union of its own heads' blocks.
+ */
+DASH_API int dash_decode_q8(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
+                            const void* v_scale, const float* ksum, const int* kv_len, void* out, int B, int Hq,
+                            int Hkv, int Tmax, int d, int block, float alpha, float coarse_scale, void* workspace,
+                            size_t ws_bytes, dash_stream_t stream);
+
+/* Bytes of workspace dash_decode_tree and dash_decode_tree_q8 need (0 when the shape is
+ * unsupported). */
+DASH_API size_t dash_decode_tree_workspace_size(int B, int Hq, int Hkv, int N, int Tmax, int d, int block);
+
+/*
+ * One decode step for a tree of N <= 64 drafted tokens per sequence.  Node i of sequence b has
+ * depth 0 (a root, parent[b, i] = -1) or its parent's depth + 1, and gets what dash_decode
+ * would give it if the tokens of its path (its ancestors, then itself) followed the kv_len[b]
+ * cached ones; its own block, the past blocks and, where the path completes the cache's open
+ * block, that block's summary (the mean of its cached keys and the path's) follow from there.
+ *   q        device bf16 [B, Hq, N, d]
+ *   k_draft, v_draft  device bf16 [B, Hkv, N, d]: the drafted tokens' keys and values
+ *   parent   device int32 [B, N], -1 <= parent[b, i] < i
+ *   n_nodes  device int32 [B] or NULL: nodes of each sequence (clamped to [0, N]; NULL: N); rows
+ *            of out behind them are left as they were
+ *   k_cache, v_cache  device bf16 [B, Hkv, Tmax, d]; rows from kv_len[b] on are not used
+ *   ksum     device fp32 [B, Hkv, Tmax / block, d]: summaries of the blocks j < kv_len[b] / block
+ *   kv_len   device int32 [B], 0 <= kv_len[b] <= Tmax (the drafted tokens need no room in the cache)
+ *   out      device bf16 [B, Hq, N, d]
+ * Nodes of a sequence with kv_len[b] outside its range, nodes whose parent lies outside
+ * [-1, i), and their descendants get zero.  At most 32 query heads per KV head;
+ * B * Hkv * Tmax < 2^31.  Cached rows before kv_len[b] and the draft rows of the nodes must be finite: a
+ * non-finite value can reach every row of its KV group.
+ */
+DASH_API int dash_decode_tree(const void* q, const void* k_draft, const void* v_draft, const int* parent,
+                              const int* n_nodes, const void* k_cache, const void* v_cache, const float* ksum,
+                              const int* kv_len, void* out, int B, int Hq, int Hkv, int N, int Tmax, int d, int block,
+                              float alpha, float coarse_scale, void* workspace, size_t ws_bytes,
+                              dash_stream_t stream);
+
+/* dash_decode_tree over the 8-bit cache.  The drafted tokens' keys and values are bf16 and are used as
+ * they are (dash_cache_append rounds the accepted ones when it writes them). */
+DASH_API int dash_decode_tree_q8(const void* q, const void* k_draft, const void* v_draft, const int* parent,
+                                 const int* n_nodes, const void* k_cache, const void* v_cache, const void* k_scale,
+                                 const void* v_scale, const float* ksum, const int* kv_len, void* out, int B, int Hq,
+                                 int Hkv, int N, int Tmax, int d, int block, float alpha, float coarse_scale,
+                                 void* workspace, size_t ws_bytes, dash_stream_t stream);
+
 /* Synchronises `stream` and returns DASH_OK, DASH_ERR_DEVICE_TIMEOUT when a kernel that used
  * `workspace` gave up a bounded wait, DASH_ERR_NO_CONVERGE when one recorded a failed
  * threshold solve, or DASH_ERR_CUDA. */

@@ -1,7 +1,8 @@
 // api.cu -- the extern "C" entry points declared in include/dash_attn.h.
 //
 // Argument checks happen here, before any launch; kernels live in summary.cu, coarse.cu,
-// coarse_tc.cu, fine_mma.cu, fine_tc.cu, backward.cu, decode.cu, decode_tc.cu and dump.cu.
+// coarse_tc.cu, fine_mma.cu, fine_tc.cu, backward.cu, decode.cu, decode_tc.cu, decode_q8.cu,
+// cache8.cu, tree.cu and dump.cu.
 // Nothing here allocates memory.
 #include <algorithm>
 #include <math.h>
@@ -23,6 +24,12 @@ inline bool al256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u
 inline cudaStream_t S(dash_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 inline bool good_params(float alpha, float cs) {
     return isfinite(alpha) && alpha > 1.0f && isfinite(cs);
+}
+
+// an 8-bit cache holds whole blocks; its rows are counted in 32 bits (int32 tensor-map coordinates)
+inline bool good_cache(int B, int Hkv, int Tmax, int d, int block) {
+    return block == kBlock && (d == 64 || d == 128) && B >= 1 && Hkv >= 1 && Tmax >= 1 && Tmax <= kMaxT &&
+           Tmax % kBlock == 0 && (long long)B * Hkv * Tmax < (1ll << 31);
 }
 
 int read_stats(const void* ws, size_t ws_bytes, dash_stats* out, dash_stream_t stream) {
@@ -446,6 +453,95 @@ int dash_decode_profiled(const void* q, const void* k_cache, const void* v_cache
     if (!events) return DASH_ERR_ARG;
     return decode_impl(q, k_cache, v_cache, ksum, kv_len, out, B, Hq, Hkv, Tmax, d, block, alpha,
                        coarse_scale, workspace, ws_bytes, stream, events);
+}
+
+// ------------------------------------------------------------------ 8-bit KV cache
+
+int dash_cache_append(const void* k_new, const void* v_new, const int* src, const int* n_new, const int* kv_len,
+                      void* k_cache, void* v_cache, void* k_scale, void* v_scale, float* ksum, int B, int Hkv,
+                      int n_rows, int n, int Tmax, int d, int block, dash_stream_t stream) {
+    if (!k_new || !v_new || !kv_len || !k_cache || !v_cache || !k_scale || !v_scale) return DASH_ERR_ARG;
+    if (!al16(k_new) || !al16(v_new) || !al16(k_cache) || !al16(v_cache) || !al16(k_scale) || !al16(v_scale) ||
+        (ksum && !al16(ksum)))
+        return DASH_ERR_ARG;
+    if (!good_cache(B, Hkv, Tmax, d, block) || n < 0 || n > Tmax || n_rows < 0 || (!src && n > n_rows)) return DASH_ERR_SHAPE;
+    return launch_cache_append(k_new, v_new, src, n_new, kv_len, k_cache, v_cache, k_scale, v_scale, ksum, B, Hkv,
+                               n_rows, n, Tmax, d, S(stream)) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+}
+
+int dash_cache_read(const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                    const int* start, const int* kv_len, void* k_out, void* v_out, int B, int Hkv, int n, int Tmax,
+                    int d, int block, dash_stream_t stream) {
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !k_out || !v_out) return DASH_ERR_ARG;
+    if (!al16(k_cache) || !al16(v_cache) || !al16(k_scale) || !al16(v_scale) || !al16(k_out) || !al16(v_out))
+        return DASH_ERR_ARG;
+    if (!good_cache(B, Hkv, Tmax, d, block) || n < 0 || n > kMaxT) return DASH_ERR_SHAPE;
+    return launch_cache_read(k_cache, v_cache, k_scale, v_scale, start, kv_len, k_out, v_out, B, Hkv, n, Tmax, d,
+                             S(stream)) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+}
+
+size_t dash_decode_q8_workspace_size(int B, int Hq, int Hkv, int Tmax, int d, int block) {
+    DecodeQ8Geom g;
+    if (block != kBlock || !make_decode_q8_geom(B, Hq, Hkv, Tmax, d, &g)) return 0;
+    return g.v.total;
+}
+
+int dash_decode_q8(const void* q, const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                   const float* ksum, const int* kv_len, void* out, int B, int Hq, int Hkv, int Tmax, int d, int block,
+                   float alpha, float coarse_scale, void* workspace, size_t ws_bytes, dash_stream_t stream) {
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !ksum || !kv_len || !out) return DASH_ERR_ARG;
+    if (!al16(q) || !al16(k_cache) || !al16(v_cache) || !al16(k_scale) || !al16(v_scale) || !al16(ksum) || !al16(out))
+        return DASH_ERR_ARG;
+    if (!good_params(alpha, coarse_scale)) return DASH_ERR_ARG;
+    DecodeQ8Geom g;
+    if (block != kBlock || !make_decode_q8_geom(B, Hq, Hkv, Tmax, d, &g)) return DASH_ERR_SHAPE;
+    if (!workspace || !al256(workspace) || ws_bytes < g.v.total) return DASH_ERR_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    if (cudaMemsetAsync(ws, 0, sizeof(WsHeader), S(stream)) != cudaSuccess) return DASH_ERR_CUDA;
+    return launch_decode_q8(q, k_cache, v_cache, k_scale, v_scale, ksum, kv_len, out, g, ws, alpha, coarse_scale,
+                            S(stream)) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ drafted-token trees
+
+size_t dash_decode_tree_workspace_size(int B, int Hq, int Hkv, int N, int Tmax, int d, int block) {
+    TreeGeom g;
+    if (block != kBlock || !make_tree_geom(B, Hq, Hkv, N, Tmax, d, &g)) return 0;
+    return g.total;
+}
+
+static int tree_impl(const TreeArgs& a, bool q8, int B, int Hq, int Hkv, int N, int Tmax, int d, int block,
+                     float alpha, float coarse_scale, void* workspace, size_t ws_bytes, dash_stream_t stream) {
+    if (!a.q || !a.k_draft || !a.v_draft || !a.parent || !a.k_cache || !a.v_cache || !a.ksum || !a.kv_len || !a.out)
+        return DASH_ERR_ARG;
+    if (!al16(a.q) || !al16(a.k_draft) || !al16(a.v_draft) || !al16(a.k_cache) || !al16(a.v_cache) || !al16(a.ksum) ||
+        !al16(a.out))
+        return DASH_ERR_ARG;
+    if (q8 && (!a.k_scale || !a.v_scale || !al16(a.k_scale) || !al16(a.v_scale))) return DASH_ERR_ARG;
+    if (!good_params(alpha, coarse_scale)) return DASH_ERR_ARG;
+    TreeGeom g;
+    if (block != kBlock || !make_tree_geom(B, Hq, Hkv, N, Tmax, d, &g) || (q8 && Tmax % kBlock)) return DASH_ERR_SHAPE;
+    if (!workspace || !al256(workspace) || ws_bytes < g.total) return DASH_ERR_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    if (cudaMemsetAsync(ws, 0, sizeof(WsHeader), S(stream)) != cudaSuccess) return DASH_ERR_CUDA;
+    return launch_tree(a, g, ws, alpha, coarse_scale, S(stream)) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+}
+
+int dash_decode_tree(const void* q, const void* k_draft, const void* v_draft, const int* parent, const int* n_nodes,
+                     const void* k_cache, const void* v_cache, const float* ksum, const int* kv_len, void* out, int B,
+                     int Hq, int Hkv, int N, int Tmax, int d, int block, float alpha, float coarse_scale,
+                     void* workspace, size_t ws_bytes, dash_stream_t stream) {
+    const TreeArgs a = {q, k_draft, v_draft, parent, n_nodes, k_cache, v_cache, nullptr, nullptr, ksum, kv_len, out};
+    return tree_impl(a, false, B, Hq, Hkv, N, Tmax, d, block, alpha, coarse_scale, workspace, ws_bytes, stream);
+}
+
+int dash_decode_tree_q8(const void* q, const void* k_draft, const void* v_draft, const int* parent,
+                        const int* n_nodes, const void* k_cache, const void* v_cache, const void* k_scale,
+                        const void* v_scale, const float* ksum, const int* kv_len, void* out, int B, int Hq, int Hkv,
+                        int N, int Tmax, int d, int block, float alpha, float coarse_scale, void* workspace,
+                        size_t ws_bytes, dash_stream_t stream) {
+    const TreeArgs a = {q, k_draft, v_draft, parent, n_nodes, k_cache, v_cache, k_scale, v_scale, ksum, kv_len, out};
+    return tree_impl(a, true, B, Hq, Hkv, N, Tmax, d, block, alpha, coarse_scale, workspace, ws_bytes, stream);
 }
 
 int dash_get_device_status(const void* workspace, dash_stream_t stream) {

@@ -96,4 +96,35 @@ cudaError_t launch_decode(const void* q, const void* kc, const void* vc, const f
                           const cudaEvent_t* events, int agg = 0, float* x_dump = nullptr,
                           float* p_dump = nullptr);
 
+// ---- 8-bit KV cache (format: cache8.cuh): writing rows (src, n_new, ksum may be null), reading
+// rows back (start, kv_len may be null)
+cudaError_t launch_cache_append(const void* k_new, const void* v_new, const int* src, const int* n_new,
+                                const int* kv_len, void* kc, void* vc, void* ks, void* vs, float* ksum, int B,
+                                int Hkv, int n_rows, int n, int Tmax, int d, cudaStream_t stream);
+cudaError_t launch_cache_read(const void* kc, const void* vc, const void* ks, const void* vs, const int* start,
+                              const int* kv_len, void* ko, void* vo, int B, int Hkv, int n, int Tmax, int d,
+                              cudaStream_t stream);
+
+// scores, thresholds, block lists and work plan (for nctas CTAs, 0: none) of a decode step:
+// scores over the KV groups of g, lists over those of gl (g itself, or its virtual groups)
+cudaError_t launch_decode_lists(const void* q, const float* ksum, const int* kv_len, void* out, const DecodeGeom& g,
+                                const DecodeGeom& gl, char* ws, float alpha, float coarse_scale, int nctas,
+                                cudaStream_t stream);
+
+// ---- decode step over the 8-bit cache
+cudaError_t launch_decode_q8(const void* q, const void* kc, const void* vc, const void* ks, const void* vs,
+                             const float* ksum, const int* kv_len, void* out, const DecodeQ8Geom& g, char* ws,
+                             float alpha, float coarse_scale, cudaStream_t stream);
+
+// ---- decode step over drafted-token trees; k_scale / v_scale null: bf16 caches, else 8-bit
+struct TreeArgs {
+    const void *q, *k_draft, *v_draft;
+    const int *parent, *n_nodes;
+    const void *k_cache, *v_cache, *k_scale, *v_scale;
+    const float* ksum;
+    const int* kv_len;
+    void* out;
+};
+cudaError_t launch_tree(const TreeArgs& a, const TreeGeom& g, char* ws, float alpha, float coarse_scale, cudaStream_t stream);
+
 }  // namespace dash

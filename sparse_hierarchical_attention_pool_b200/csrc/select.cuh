@@ -1,0 +1,177 @@
+// select.cuh -- threshold solves with one warp per row, and the work plan of the balanced
+// split-KV pass: shared by the decode steps (decode.cu, tree.cu).
+#pragma once
+
+#include "common.cuh"
+#include "entmax.cuh"
+
+namespace dash {
+
+constexpr int kSelRegs = 48;        // row values a select lane keeps in registers
+
+// Row values of one head on one warp: lane l holds x[l + 32 k] for k < kSelRegs in
+// registers (-inf past the row's end, which no pass counts); values past that are read from
+// memory.
+struct WarpRow {
+    float r[kSelRegs];
+    const float* p;
+    int lane, n;
+    __device__ __forceinline__ void load(const float* row, int ln, int count) {
+        p = row; lane = ln; n = count;
+#pragma unroll
+        for (int k = 0; k < kSelRegs; ++k) {
+            const int j = lane + 32 * k;
+            r[k] = j < n ? row[j] : -INFINITY;
+        }
+    }
+    template <class F>
+    __device__ __forceinline__ void each(F&& f) const {
+#pragma unroll
+        for (int k = 0; k < kSelRegs; ++k) f(lane + 32 * k, r[k]);
+        for (int j = lane + 32 * kSelRegs; j < n; j += 32) f(j, p[j]);
+    }
+};
+
+constexpr int kHistBins = 64;       // bins of the histogram start over y = x - m in [-1, 0)
+
+// Histogram start of the threshold solve (the idea of AdaSplash-2, whose abstract appears on
+// the listing page "DashAttention: Differentiable and Adaptive Sparse Hierarchical Attention":
+// a coarse histogram of the scores kept in on-chip memory gives a close initial threshold;
+// the construction here is this library's):
+// the values y = x - m in [-1, 0) go to bin k = floor((y + 1) * 64) with their count, sum and
+// sum of squares, accumulated as integers (y and y^2 in 2^-24 fixed point), so the sums and
+// the start do not depend on the order of the shared-memory atomics.  At a bin's lower edge
+// e every value of the bins above lies above e, so f(e) = sum_{y > e} (y - e)^(1/(alpha-1))
+// is exact there for alpha = 1.5 (S2 - 2 e S1 + e^2 S0) and alpha = 2 (S1 - e S0).  f is
+// decreasing, so the highest edge with f >= 1 lies just below the root: Newton starts there
+// instead of at -1.
+// bins: this warp's shared area (kHistBins counts, then kHistBins sums, kHistBins sums of
+// squares).  Every lane returns the start.
+struct HistBins {
+    unsigned int c[kHistBins];
+    unsigned long long s1[kHistBins], s2[kHistBins];
+};
+
+template <int MODE>
+__device__ __forceinline__ float hist_start(const WarpRow& xr, float m, HistBins* hb) {
+    const int lane = threadIdx.x & 31;
+    constexpr float kFix = 16777216.0f;                 // 2^24
+    for (int i = lane; i < kHistBins; i += 32) { hb->c[i] = 0u; hb->s1[i] = 0ull; hb->s2[i] = 0ull; }
+    __syncwarp();
+    xr.each([&](int, float v) {
+        const float y = v - m;
+        if (y > -1.0f) {
+            const int k = min(kHistBins - 1, (int)((y + 1.0f) * (float)kHistBins));
+            atomicAdd(&hb->c[k], 1u);
+            atomicAdd(&hb->s1[k], (unsigned long long)__float2ll_rn(y * kFix));
+            atomicAdd(&hb->s2[k], (unsigned long long)__float2ll_rn(y * y * kFix));
+        }
+    });
+    __syncwarp();
+    // lane l holds bins 2l, 2l + 1; exact suffix sums over the bins at and above each edge
+    long long c0 = hb->c[2 * lane], c1 = hb->c[2 * lane + 1];
+    long long p0 = (long long)hb->s1[2 * lane], p1 = (long long)hb->s1[2 * lane + 1];
+    long long q0 = (long long)hb->s2[2 * lane], q1 = (long long)hb->s2[2 * lane + 1];
+    long long ac = c0 + c1, a1 = p0 + p1, a2 = q0 + q1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long nc = __shfl_down_sync(0xffffffffu, ac, o);
+        const long long n1 = __shfl_down_sync(0xffffffffu, a1, o);
+        const long long n2 = __shfl_down_sync(0xffffffffu, a2, o);
+        if (lane + o < 32) { ac += nc; a1 += n1; a2 += n2; }
+    }
+    auto f_at = [&](int k, long long S0, long long S1q, long long S2q) {
+        const double e = -1.0 + (double)k / kHistBins;
+        const double S1 = (double)S1q / kFix, S2 = (double)S2q / kFix;
+        return MODE == 1 ? S2 - 2.0 * e * S1 + e * e * (double)S0 : S1 - e * (double)S0;
+    };
+    const unsigned ok_odd = __ballot_sync(0xffffffffu, f_at(2 * lane + 1, ac - c0, a1 - p0, a2 - q0) >= 1.0);
+    const unsigned ok_even = __ballot_sync(0xffffffffu, f_at(2 * lane, ac, a1, a2) >= 1.0);
+    const int k_odd = ok_odd ? 2 * (31 - __clz((int)ok_odd)) + 1 : -1;
+    const int k_even = ok_even ? 2 * (31 - __clz((int)ok_even)) : 0;
+    __syncwarp();
+    return -1.0f + (float)max(k_odd, k_even) / (float)kHistBins;
+}
+
+// Threshold of one row held by a warp (every lane returns it); MODE as in EntmaxPass::add_t.
+// bins != nullptr: start from the histogram edge (alpha = 1.5 and 2), else from u = -1.
+template <int MODE>
+__device__ __forceinline__ float warp_row_tau(const WarpRow& xr, float m, float alpha, int* no_conv,
+                                              HistBins* bins, int cap) {
+    float u0 = -1.0f;
+    if constexpr (MODE != 0) {
+        if (bins) u0 = hist_start<MODE>(xr, m, bins);
+    }
+    EntmaxSolver sv;
+    sv.init(m, alpha, u0, cap);
+    float t = m;
+    while (true) {
+        EntmaxPass ps;
+        ps.reset();
+        xr.each([&](int, float v) { ps.add_t<MODE>((v - sv.m) - sv.u, sv.e); });
+        ps.warp_reduce_t<MODE>();
+        if (sv.update(ps, &t, no_conv)) break;
+    }
+    return t;
+}
+
+// Work plan of the balanced attention pass, built by the last select CTA to finish (a
+// ticket in the workspace header): offs = exclusive prefix of the list lengths (U = offs[BH]
+// blocks in all), and plan[c] = the group holding position floor(U c / n), where CTA c's
+// range starts (n = min(nctas, U)).  Called by every thread of every CTA once its count is
+// written.
+static __device__ void decode_plan_tail(const int* count, int* offs, int* plan, WsHeader* hdr, int BH, int nctas) {
+    __shared__ int last_sh;
+    __shared__ int wsum[32];
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();                              // this CTA's count before its ticket
+        last_sh = atomicAdd(&hdr->ticket, 1) == BH - 1;
+    }
+    __syncthreads();
+    if (!last_sh) return;
+    __threadfence();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarp = blockDim.x >> 5;
+    const int slice = (BH + nwarp - 1) / nwarp;
+    const int lo = min(BH, warp * slice), hi = min(BH, lo + slice);
+    int sum = 0;
+    for (int i = lo + lane; i < hi; i += 32) sum += __ldcg(count + i);
+    sum = warp_sum_int(sum);
+    if (lane == 0) wsum[warp] = sum;
+    __syncthreads();
+    int before = 0, U = 0;
+    for (int w = 0; w < nwarp; ++w) {
+        if (w < warp) before += wsum[w];
+        U += wsum[w];
+    }
+    if (threadIdx.x == 0) offs[BH] = U;
+    if (U < nctas) nctas = U;                         // the attention pass uses min(grid, U) CTAs
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int i = i0 + lane;
+        const int v = i < hi ? __ldcg(count + i) : 0;
+        int incl = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += n;
+        }
+        const int o0 = before + incl - v, o1 = before + incl;
+        if (i < hi) {
+            offs[i] = o0;
+            if (v > 0) {
+                // CTAs whose range starts inside [o0, o1)
+                const int c_lo = (int)(((long long)o0 * nctas + U - 1) / U);
+                const int c_hi = (int)(((long long)o1 * nctas - 1) / U);
+                for (int c = c_lo; c <= c_hi; ++c) plan[c] = i;
+            }
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+// The CTA whose range [U c / n, U (c + 1) / n) holds list position pos.
+__device__ __forceinline__ int dt_cta_of(long long pos, long long U, int n) {
+    return (int)(((pos + 1) * n - 1) / U);
+}
+
+}  // namespace dash

@@ -29,7 +29,9 @@ EXPORTS = ("dash_status_string", "dash_version", "dash_block_summary", "dash_pre
            "dash_get_device_status", "dash_prefill_profiled", "dash_decode_profiled",
            "dash_decode_noalloc", "dash_decode_noalloc_status", "dash_block_summary_w", "dash_prefill_w", "dash_prefill_ex",
            "dash_decode_ex", "dash_prefill_backward_workspace_size", "dash_prefill_backward",
-           "dash_prefill_dump", "dash_decode_dump")
+           "dash_prefill_dump", "dash_decode_dump", "dash_cache_append", "dash_cache_read",
+           "dash_decode_q8_workspace_size", "dash_decode_q8", "dash_decode_tree_workspace_size",
+           "dash_decode_tree", "dash_decode_tree_q8")
 
 HEAD_AGGREGATION = 1       # flag of dash_prefill_ex / dash_decode_ex
 
@@ -91,9 +93,17 @@ def lib():
     L.dash_decode_noalloc_status.argtypes = [_p]
     L.dash_prefill_dump.argtypes = [_p] * 5 + [_i] * 6 + [_f, _f, ctypes.c_uint, _p, _i, _p, _p, _p, _sz, _p]
     L.dash_decode_dump.argtypes = [_p] * 6 + [_i] * 6 + [_f, _f, ctypes.c_uint, _p, _p, _p, _p, _sz, _p]
+    L.dash_cache_append.argtypes = [_p] * 10 + [_i] * 7 + [_p]
+    L.dash_cache_read.argtypes = [_p] * 8 + [_i] * 6 + [_p]
+    L.dash_decode_q8_workspace_size.argtypes = [_i] * 6
+    L.dash_decode_q8_workspace_size.restype = _sz
+    L.dash_decode_q8.argtypes = [_p] * 8 + [_i] * 6 + [_f, _f, _p, _sz, _p]
+    L.dash_decode_tree_workspace_size.argtypes = [_i] * 7
+    L.dash_decode_tree_workspace_size.restype = _sz
+    L.dash_decode_tree.argtypes = [_p] * 10 + [_i] * 7 + [_f, _f, _p, _sz, _p]
+    L.dash_decode_tree_q8.argtypes = [_p] * 12 + [_i] * 7 + [_f, _f, _p, _sz, _p]
     for name in EXPORTS:
-        if name not in ("dash_status_string", "dash_prefill_workspace_size", "dash_decode_workspace_size",
-                        "dash_prefill_backward_workspace_size"):
+        if name != "dash_status_string" and not name.endswith("_workspace_size"):
             getattr(L, name).restype = _i
     _lib = L
     return L
@@ -481,6 +491,202 @@ def dash_prefill_backward(q, k, v, out, dout, alpha=1.5, coarse_scale=1.0, dq=No
         _stream(stream))
     _check("dash_prefill_backward", rc)
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- 8-bit KV cache, drafted trees
+
+_U8 = torch.uint8
+_E4M3 = torch.float8_e4m3fn
+
+
+class _On:
+    """The current device set to the tensors' one for a call (they must all share it)."""
+
+    def __init__(self, *tensors):
+        devs = {t.device for t in tensors if isinstance(t, torch.Tensor)}
+        if len(devs) != 1:
+            raise ValueError(f"tensors on more than one device: {sorted(map(str, devs))}")
+        dev = devs.pop()
+        if dev.type != "cuda":
+            raise ValueError("tensors must be CUDA tensors")
+        self.guard = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+
+    def __enter__(self):
+        if self.guard:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard:
+            self.guard.__exit__(*exc)
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _lens(t, B, name):
+    """An optional int32 [B] device argument."""
+    if t is None:
+        return None
+    _shape(t, (B,), name)
+    return _dev(t, torch.int32, name)
+
+
+def _cache8(k_cache, v_cache, k_scale, v_scale):
+    B, Hkv, Tmax, d = k_cache.shape
+    _shape(v_cache, (B, Hkv, Tmax, d), "v_cache")
+    _shape(k_scale, (B, Hkv, Tmax), "k_scale")
+    _shape(v_scale, (B, Hkv, Tmax), "v_scale")
+    return (_dev(k_cache, _E4M3, "k_cache"), _dev(v_cache, _E4M3, "v_cache"), _dev(k_scale, _U8, "k_scale"),
+            _dev(v_scale, _U8, "v_scale"))
+
+
+def _ksum(ksum, B, Hkv, Tmax, d, block):
+    """Block summaries [B, Hkv, Tmax // block, d] (one row at least, as dash_block_summary makes them)."""
+    if tuple(ksum.shape) not in {(B, Hkv, Tmax // block, d), (B, Hkv, max(Tmax // block, 1), d)}:
+        raise ValueError(f"ksum must be [B, Hkv, Tmax // {block}, d], got {list(ksum.shape)}")
+    return _dev(ksum, torch.float32, "ksum")
+
+
+def _space(workspace, need, device):
+    if workspace is None:
+        return alloc_workspace(need, device)
+    if workspace.device != device or workspace.dtype != _U8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
+    return workspace
+
+
+def dash_cache_alloc(B, Hkv, Tmax, d, device="cuda"):
+    """An empty 8-bit KV cache: (k_cache, v_cache float8_e4m3fn [B, Hkv, Tmax, d], k_scale, v_scale
+    uint8 [B, Hkv, Tmax], ksum fp32 [B, Hkv, Tmax // 64, d]).  Tmax must be a multiple of 64."""
+    if Tmax < 64 or Tmax % 64:
+        raise ValueError("Tmax must be a positive multiple of 64")
+    cache = [torch.zeros(B, Hkv, Tmax, d, dtype=_U8, device=device).view(_E4M3) for _ in range(2)]
+    scale = [torch.zeros(B, Hkv, Tmax, dtype=_U8, device=device) for _ in range(2)]
+    return (*cache, *scale, torch.zeros(B, Hkv, Tmax // 64, d, device=device))
+
+
+def dash_cache_append(k_new, v_new, kv_len, k_cache, v_cache, k_scale, v_scale, ksum=None, n=None, n_new=None,
+                      src=None, block=64, stream=None):
+    """Append rows to the 8-bit cache at positions kv_len[b].. and complete the summaries.
+
+    k_new, v_new bf16 [B, Hkv, rows, d]; kv_len int32 [B] (tokens held before; not changed).
+    n: tokens per sequence (default: all rows, or src's width); n_new int32 [B]: fewer for some
+    sequences; src int32 [B, n]: the row each token comes from (the accepted path of a tree).
+    ksum fp32 [B, Hkv, Tmax // 64, d] or None: the blocks this completes get their means."""
+    B, Hkv, rows, d = k_new.shape
+    Tmax = k_cache.shape[2]
+    _shape(v_new, k_new.shape, "v_new")
+    _shape(k_cache, (B, Hkv, Tmax, d), "k_cache")
+    if src is not None:
+        n = src.shape[1] if n is None else n
+        _shape(src, (B, n), "src")
+    n = rows if n is None else n
+    with _On(k_new, v_new, kv_len, k_cache, v_cache, k_scale, v_scale, ksum, n_new, src):
+        kc, vc, ks, vs = _cache8(k_cache, v_cache, k_scale, v_scale)
+        _check("dash_cache_append", lib().dash_cache_append(
+            _dev(k_new, torch.bfloat16, "k_new"), _dev(v_new, torch.bfloat16, "v_new"),
+            None if src is None else _dev(src, torch.int32, "src"), _lens(n_new, B, "n_new"),
+            _lens(kv_len, B, "kv_len"), kc, vc, ks, vs,
+            None if ksum is None else _ksum(ksum, B, Hkv, Tmax, d, block), B, Hkv, rows, n, Tmax, d, block,
+            _stream(stream)))
+
+
+def dash_cache_read(k_cache, v_cache, k_scale, v_scale, n, start=None, kv_len=None, k_out=None, v_out=None,
+                    block=64, stream=None):
+    """Rows start[b] .. start[b] + n - 1 of the 8-bit cache as bf16 (k, v) [B, Hkv, n, d]; rows at or
+    behind kv_len[b] are zero.  start, kv_len int32 [B] (None: 0 and Tmax)."""
+    B, Hkv, Tmax, d = k_cache.shape
+    k_out = torch.empty(B, Hkv, n, d, dtype=torch.bfloat16, device=k_cache.device) if k_out is None else k_out
+    v_out = torch.empty(B, Hkv, n, d, dtype=torch.bfloat16, device=k_cache.device) if v_out is None else v_out
+    _shape(k_out, (B, Hkv, n, d), "k_out")
+    _shape(v_out, (B, Hkv, n, d), "v_out")
+    if n == 0:
+        return k_out, v_out
+    with _On(k_cache, v_cache, k_scale, v_scale, start, kv_len, k_out, v_out):
+        _check("dash_cache_read", lib().dash_cache_read(
+            *_cache8(k_cache, v_cache, k_scale, v_scale), _lens(start, B, "start"), _lens(kv_len, B, "kv_len"),
+            _dev(k_out, torch.bfloat16, "k_out"), _dev(v_out, torch.bfloat16, "v_out"), B, Hkv, n, Tmax, d, block,
+            _stream(stream)))
+    return k_out, v_out
+
+
+def decode_q8_workspace_size(B, Hq, Hkv, Tmax, d, block=64) -> int:
+    n = lib().dash_decode_q8_workspace_size(B, Hq, Hkv, Tmax, d, block)
+    if n == 0:
+        raise DashError("dash_decode_q8_workspace_size", -2)
+    return n
+
+
+def decode_tree_workspace_size(B, Hq, Hkv, N, Tmax, d, block=64) -> int:
+    n = lib().dash_decode_tree_workspace_size(B, Hq, Hkv, N, Tmax, d, block)
+    if n == 0:
+        raise DashError("dash_decode_tree_workspace_size", -2)
+    return n
+
+
+def dash_decode_q8(q, k_cache, v_cache, k_scale, v_scale, ksum, kv_len, out=None, alpha=1.5, coarse_scale=1.0,
+                   workspace=None, block=64, stream=None):
+    """One decode step over the 8-bit cache: q bf16 [B, Hq, d].  Returns (out, workspace)."""
+    B, Hq, d = q.shape
+    Hkv, Tmax = k_cache.shape[1], k_cache.shape[2]
+    _shape(k_cache, (B, Hkv, Tmax, d), "k_cache")
+    out = torch.empty_like(q) if out is None else out
+    _shape(out, q.shape, "out")
+    with _On(q, k_cache, v_cache, k_scale, v_scale, ksum, kv_len, out):
+        if workspace is None or workspace.device != q.device or workspace.dtype != _U8:
+            workspace = _space(workspace, decode_q8_workspace_size(B, Hq, Hkv, Tmax, d, block), q.device)
+        _check("dash_decode_q8", lib().dash_decode_q8(
+            _dev(q, torch.bfloat16, "q"), *_cache8(k_cache, v_cache, k_scale, v_scale),
+            _ksum(ksum, B, Hkv, Tmax, d, block), _lens(kv_len, B, "kv_len"), _dev(out, torch.bfloat16, "out"),
+            B, Hq, Hkv, Tmax, d, block, float(alpha), float(coarse_scale),
+            ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _stream(stream)))
+    return out, workspace
+
+
+def _tree(name, q, k_draft, v_draft, parent, k_cache, v_cache, scales, ksum, kv_len, n_nodes, out, alpha,
+          coarse_scale, workspace, block, stream):
+    B, Hq, N, d = q.shape
+    Hkv, Tmax = k_cache.shape[1], k_cache.shape[2]
+    _shape(k_cache, (B, Hkv, Tmax, d), "k_cache")
+    _shape(v_cache, (B, Hkv, Tmax, d), "v_cache")
+    _shape(k_draft, (B, Hkv, N, d), "k_draft")
+    _shape(v_draft, (B, Hkv, N, d), "v_draft")
+    _shape(parent, (B, N), "parent")
+    out = torch.empty_like(q) if out is None else out
+    _shape(out, q.shape, "out")
+    with _On(q, k_draft, v_draft, parent, k_cache, v_cache, *scales, ksum, kv_len, n_nodes, out):
+        if workspace is None or workspace.device != q.device or workspace.dtype != _U8:
+            workspace = _space(workspace, decode_tree_workspace_size(B, Hq, Hkv, N, Tmax, d, block), q.device)
+        cache = _cache8(k_cache, v_cache, *scales) if scales else (
+            _dev(k_cache, torch.bfloat16, "k_cache"), _dev(v_cache, torch.bfloat16, "v_cache"))
+        _check(name, getattr(lib(), name)(
+            _dev(q, torch.bfloat16, "q"), _dev(k_draft, torch.bfloat16, "k_draft"),
+            _dev(v_draft, torch.bfloat16, "v_draft"), _dev(parent, torch.int32, "parent"),
+            _lens(n_nodes, B, "n_nodes"), *cache, _ksum(ksum, B, Hkv, Tmax, d, block), _lens(kv_len, B, "kv_len"),
+            _dev(out, torch.bfloat16, "out"), B, Hq, Hkv, N, Tmax, d, block, float(alpha), float(coarse_scale),
+            ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _stream(stream)))
+    return out, workspace
+
+
+def dash_decode_tree(q, k_draft, v_draft, parent, k_cache, v_cache, ksum, kv_len, n_nodes=None, out=None,
+                     alpha=1.5, coarse_scale=1.0, workspace=None, block=64, stream=None):
+    """One decode step for a tree of N drafted tokens per sequence over bf16 caches.
+
+    q bf16 [B, Hq, N, d], k_draft, v_draft bf16 [B, Hkv, N, d], parent int32 [B, N] (-1: a root, else
+    an earlier node), kv_len int32 [B] cached tokens, n_nodes int32 [B] or None.  Node i's row is what
+    dash_decode would return with the tokens of its path appended.  Returns (out, workspace)."""
+    return _tree("dash_decode_tree", q, k_draft, v_draft, parent, k_cache, v_cache, (), ksum, kv_len, n_nodes,
+                 out, alpha, coarse_scale, workspace, block, stream)
+
+
+def dash_decode_tree_q8(q, k_draft, v_draft, parent, k_cache, v_cache, k_scale, v_scale, ksum, kv_len,
+                        n_nodes=None, out=None, alpha=1.5, coarse_scale=1.0, workspace=None, block=64,
+                        stream=None):
+    """dash_decode_tree over the 8-bit cache (the drafted keys and values stay bf16)."""
+    return _tree("dash_decode_tree_q8", q, k_draft, v_draft, parent, k_cache, v_cache, (k_scale, v_scale), ksum,
+                 kv_len, n_nodes, out, alpha, coarse_scale, workspace, block, stream)
 
 
 class DashAttentionFunction(torch.autograd.Function):
