@@ -120,7 +120,15 @@ __device__ __forceinline__ float warp_row_tau(const WarpRow& xr, float m, float 
 // blocks in all), and plan[c] = the group holding position floor(U c / n), where CTA c's
 // range starts (n = min(nctas, U)).  Called by every thread of every CTA once its count is
 // written.
-static __device__ void decode_plan_tail(const int* count, int* offs, int* plan, WsHeader* hdr, int BH, int nctas) {
+// CTAs that share U blocks: at most `grid`, and (per > 1) at least `per` blocks each where U
+// allows, so that short lists are not cut into pieces whose merge costs more than they save.
+__host__ __device__ inline int split_ctas(long long U, int grid, int per) {
+    const long long n = per > 1 ? (U + per - 1) / per : U;
+    return (int)(n < (long long)grid ? n : (long long)grid);
+}
+
+static __device__ void decode_plan_tail(const int* count, int* offs, int* plan, WsHeader* hdr, int BH, int nctas,
+                                        int per = 1) {
     __shared__ int last_sh;
     __shared__ int wsum[32];
     __syncthreads();
@@ -145,7 +153,7 @@ static __device__ void decode_plan_tail(const int* count, int* offs, int* plan, 
         U += wsum[w];
     }
     if (threadIdx.x == 0) offs[BH] = U;
-    if (U < nctas) nctas = U;                         // the attention pass uses min(grid, U) CTAs
+    nctas = split_ctas(U, nctas, per);
     for (int i0 = lo; i0 < hi; i0 += 32) {
         const int i = i0 + lane;
         const int v = i < hi ? __ldcg(count + i) : 0;

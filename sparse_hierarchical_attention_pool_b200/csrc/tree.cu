@@ -17,22 +17,15 @@
 //                    CTA per KV group the ancestor masks, depths and the open block's scores;
 //   2. tree_select : thresholds (one warp per row), the union of every tile's selected blocks,
 //                    and the work plan;
-//   3. attention   : every row over its selected blocks, the open block and its path.
+//   3. tree_attn, tree_combine (tree_tc.cu): every row over its selected blocks, the open block and
+//                    its path.
 #include "cache8.cuh"
 #include "kernels.h"
 #include "mma_sync.cuh"
 #include "select.cuh"
+#include "tree.cuh"
 
 namespace dash {
-
-constexpr int kTreeOpen = -1, kTreeDraft = -2;   // list entries behind the past blocks
-
-// Whether the sequence's length is valid, and how many of its nodes are computed.
-__device__ __forceinline__ bool tree_live(const int* kv_len, const int* n_nodes, const TreeGeom& g, int b, int* L, int* nodes) {
-    *L = kv_len[b];
-    *nodes = n_nodes ? max(0, min(n_nodes[b], g.N)) : g.N;
-    return *L >= 0 && *L <= g.Tmax && *nodes > 0;
-}
 
 // ------------------------------------------------------------------ scores
 //
@@ -95,7 +88,7 @@ tree_scores_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __r
                    const int* __restrict__ parent, const int* __restrict__ n_nodes, const void* __restrict__ kc,
                    const uint8_t* __restrict__ ks, const float* __restrict__ ksum, const int* __restrict__ kv_len,
                    float* __restrict__ xs, unsigned long long* __restrict__ anc, int* __restrict__ depth,
-                   unsigned* __restrict__ bits, int* __restrict__ tick, int* __restrict__ done, TreeGeom g, float cx) {
+                   unsigned* __restrict__ bits, int* __restrict__ tick, TreeGeom g, float cx) {
     __shared__ int par_s[kMaxNodes], dep_s[kMaxNodes];
     __shared__ float path[kMaxNodes][D];
     const int bg = blockIdx.x, b = bg / g.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -109,7 +102,7 @@ tree_scores_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __r
     }
     // the group's tiles start with nothing selected
     for (int i = tid; i < g.tiles_bg * g.nbw; i += 128) bits[(size_t)bg * g.tiles_bg * g.nbw + i] = 0u;
-    for (int i = tid; i < g.tiles_bg; i += 128) { tick[bg * g.tiles_bg + i] = 0; done[bg * g.tiles_bg + i] = 0; }
+    for (int i = tid; i < g.tiles_bg; i += 128) tick[bg * g.tiles_bg + i] = 0;
     // ancestor sets and depths: every node walks up its path (parents come before children, so
     // the walk ends); a parent outside [-1, i) makes the node and its descendants invalid
     for (int i = tid; i < nodes; i += 128) par_s[i] = parent[(size_t)b * g.N + i];
@@ -188,7 +181,7 @@ tree_select_kernel(const int* __restrict__ kv_len, const int* __restrict__ n_nod
                    const unsigned long long* __restrict__ anc, const int* __restrict__ depth, float* __restrict__ tau,
                    unsigned* __restrict__ bits, int* __restrict__ tick, int* __restrict__ list, int* __restrict__ count,
                    int* __restrict__ offs, int* __restrict__ plan, __nv_bfloat16* __restrict__ out,
-                   WsHeader* __restrict__ hdr, TreeGeom g, float alpha, int nctas) {
+                   WsHeader* __restrict__ hdr, TreeGeom g, float alpha, int nctas, int per) {
     __shared__ int last_sh, wtot[kTreeSelWarps];
     constexpr int kCtasPerTile = kTreeRows / kTreeSelWarps;
     const int tile = blockIdx.x / kCtasPerTile, sub = blockIdx.x % kCtasPerTile;
@@ -284,132 +277,18 @@ tree_select_kernel(const int* __restrict__ kv_len, const int* __restrict__ n_nod
         }
     }
     if (tid == 0) count[tile] = total;
-    decode_plan_tail(count, offs, plan, hdr, g.tiles, nctas);
+    decode_plan_tail(count, offs, plan, hdr, g.tiles, nctas, per);
 }
 
-// ------------------------------------------------------------------ attention
-//
-// One CTA of four warps per row; warp w takes every fourth of the row's entries, a lane two of
-// the entry's 64 keys, and keeps its own running maximum, sum and output; merged at the end.
-template <int D, bool Q8>
-__device__ __forceinline__ void tree_row_kv(const void* c, const uint8_t* s, size_t row, int dim, float* o) {
-    if constexpr (Q8) {
-        e4m3x4_to_float(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(c) + row * D + dim), scale_value(s[row]), o);
-    } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(c) + row * D + dim);
-        const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-        o[0] = a.x; o[1] = a.y; o[2] = b.x; o[3] = b.y;
-    }
-}
+// ------------------------------------------------------------------ host side
 
-template <int D>
-struct RowState {
-    float m, l, o[D / 32];
-    __device__ __forceinline__ void reset() {
-        m = -INFINITY; l = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-    }
-};
+constexpr int kTreePer = 4;          // list entries per CTA at least
 
-// 64 keys from row k0; lane's keys lane and lane + 32 have log2 priors lp[0], lp[1] (-inf: not
-// attended, and not read)
-template <int D, bool Q8>
-__device__ void tree_row_block(RowState<D>& st, const float* qs, const void* kc, const uint8_t* ks, const void* vc,
-                               const uint8_t* vs, size_t k0, const float* lp, float sm2) {
-    const int lane = threadIdx.x & 31;
-    float s[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        s[h] = -INFINITY;
-        if (lp[h] > -INFINITY) {
-            float acc = 0.f;
-            for (int c = 0; c < D; c += 4) {
-                float f[4];
-                tree_row_kv<D, Q8>(kc, ks, k0 + lane + 32 * h, c, f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc = fmaf(qs[c + i], f[i], acc);
-            }
-            s[h] = fmaf(acc, sm2, lp[h]);
-        }
-    }
-    const float mn = fmaxf(st.m, warp_max(fmaxf(s[0], s[1])));
-    if (mn == -INFINITY) return;
-    const float sc = exp2f(st.m - mn);
-    const float p0 = exp2f(s[0] - mn), p1 = exp2f(s[1] - mn);
-    st.m = mn;
-    st.l = st.l * sc + warp_sum(p0 + p1);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) st.o[i] *= sc;
-    for (int key = 0; key < 64; ++key) {
-        const float p = __shfl_sync(0xffffffffu, key < 32 ? p0 : p1, key & 31);
-        if (p == 0.f) continue;
-        float f[4];
-        const int dim = lane * (D / 32);
-        tree_row_kv<D, Q8>(vc, vs, k0 + key, dim & ~3, f);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) st.o[i] = fmaf(p, f[(dim & 3) + i], st.o[i]);
-    }
-}
-
-template <int D, bool Q8>
-__global__ void __launch_bounds__(128)
-tree_row_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ kd,
-                const __nv_bfloat16* __restrict__ vd, const int* __restrict__ n_nodes, const void* __restrict__ kc,
-                const void* __restrict__ vc, const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vs,
-                const int* __restrict__ kv_len, const float* __restrict__ xs, const float* __restrict__ tau,
-                const unsigned long long* __restrict__ anc, const int* __restrict__ depth,
-                __nv_bfloat16* __restrict__ out, TreeGeom g, float e_pow, float sm2) {
-    __shared__ float qs[D], ms[4], lsum[4], os[4][D];
-    const size_t row = blockIdx.x;
-    const int bg = (int)(row / g.R), b = bg / g.Hkv, node = (int)(row % g.N);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int L, nodes;
-    if (!tree_live(kv_len, n_nodes, g, b, &L, &nodes) || node >= nodes) return;
-    const unsigned long long a = anc[(size_t)b * g.N + node];
-    if (!a) return;
-    const int F = L / kBlock, r = L % kBlock, dp = depth[(size_t)b * g.N + node];
-    for (int c = tid; c < D; c += 128) qs[c] = __bfloat162float(q[row * D + c]);
-    __syncthreads();
-    RowState<D> st;
-    st.reset();
-    const float* x = xs + row * g.cap;
-    const float t = tau[row];
-    const size_t k0 = (size_t)bg * g.Tmax;
-    for (int j = warp; j < F; j += 4) {
-        if (!(x[j] > t)) continue;
-        const float v = e_pow * __log2f(x[j] - t);
-        const float lp[2] = {v, v};
-        tree_row_block<D, Q8>(st, qs, kc, ks, vc, vs, k0 + (size_t)j * kBlock, lp, sm2);
-    }
-    // the open block's prior: 1, or its weight once the path has completed it
-    const bool crossed = r + dp >= kBlock;
-    const float lpo = !crossed ? 0.f : x[F] > t ? e_pow * __log2f(x[F] - t) : -INFINITY;
-    if (warp == 0 && r > 0) {
-        const float lp[2] = {lane < r ? lpo : -INFINITY, lane + 32 < r ? lpo : -INFINITY};
-        tree_row_block<D, Q8>(st, qs, kc, ks, vc, vs, k0 + (size_t)F * kBlock, lp, sm2);
-    }
-    if (warp == 1) {
-        float lp[2];
-        for (int h = 0; h < 2; ++h) {
-            const int i = lane + 32 * h;
-            lp[h] = (a >> i) & 1ull ? (crossed && r + depth[(size_t)b * g.N + i] < kBlock ? lpo : 0.f) : -INFINITY;
-        }
-        tree_row_block<D, false>(st, qs, kd, nullptr, vd, nullptr, (size_t)bg * g.N, lp, sm2);
-    }
-    if (lane == 0) { ms[warp] = st.m; lsum[warp] = st.l; }
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) os[warp][lane * (D / 32) + i] = st.o[i];
-    __syncthreads();
-    const float M = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
-    float den = 0.f;
-    for (int w = 0; w < 4; ++w) den = fmaf(lsum[w], exp2f(ms[w] - M), den);
-    for (int c = tid; c < D; c += 128) {
-        float num = 0.f;
-        for (int w = 0; w < 4; ++w) num = fmaf(os[w][c], exp2f(ms[w] - M), num);
-        out[row * D + c] = __float2bfloat16(num / den);
-    }
+// one CTA per SM (its operand rings fill the shared memory)
+static int tree_ctas() {
+    int dev = 0, n = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n < 1 ? 1 : n < kDecodeMaxCtas ? n : kDecodeMaxCtas;
 }
 
 template <int D, bool Q8>
@@ -417,32 +296,21 @@ static cudaError_t launch_tree_t(const TreeArgs& a, const TreeGeom& g, char* ws,
                                  cudaStream_t stream) {
     const float cx = (alpha - 1.0f) * coarse_scale / sqrtf((float)D);
     const float e_pow = 1.0f / (alpha - 1.0f), sm2 = 1.4426950408889634f / sqrtf((float)D);
-    float* xs = reinterpret_cast<float*>(ws + g.off_x);
-    float* tau = reinterpret_cast<float*>(ws + g.off_tau);
-    auto* anc = reinterpret_cast<unsigned long long*>(ws + g.off_anc);
-    int* depth = reinterpret_cast<int*>(ws + g.off_depth);
-    unsigned* bits = reinterpret_cast<unsigned*>(ws + g.off_bits);
-    int* tick = reinterpret_cast<int*>(ws + g.off_tick);
-    int* list = reinterpret_cast<int*>(ws + g.off_list);
-    int* count = reinterpret_cast<int*>(ws + g.off_count);
-    int* done = reinterpret_cast<int*>(ws + g.off_done);
-    int* offs = reinterpret_cast<int*>(ws + g.off_offs);
-    int* plan = reinterpret_cast<int*>(ws + g.off_plan);
-    WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
+    const TreeWork w = tree_work(g, ws);
     const auto* q = static_cast<const __nv_bfloat16*>(a.q);
     const auto* kd = static_cast<const __nv_bfloat16*>(a.k_draft);
-    const auto* vd = static_cast<const __nv_bfloat16*>(a.v_draft);
     const auto* ks = static_cast<const uint8_t*>(a.k_scale);
-    const auto* vs = static_cast<const uint8_t*>(a.v_scale);
     auto* out = static_cast<__nv_bfloat16*>(a.out);
     const dim3 gs((unsigned)(g.B * g.Hkv), (unsigned)((g.nbs + 63) / 64 + 1));
-    tree_scores_kernel<D, Q8><<<gs, 128, 0, stream>>>(q, kd, a.parent, a.n_nodes, a.k_cache, ks, a.ksum, a.kv_len, xs, anc,
-                                                      depth, bits, tick, done, g, cx);
+    const int nctas = tree_ctas();
+    tree_scores_kernel<D, Q8><<<gs, 128, 0, stream>>>(q, kd, a.parent, a.n_nodes, a.k_cache, ks, a.ksum, a.kv_len, w.xs, w.anc,
+                                                      w.depth, w.bits, w.tick, g, cx);
     tree_select_kernel<<<(unsigned)g.tiles * (kTreeRows / kTreeSelWarps), kTreeSelWarps * 32, 0, stream>>>(
-        a.kv_len, a.n_nodes, xs, anc, depth, tau, bits, tick, list, count, offs, plan, out, hdr, g, alpha, 148);
-    tree_row_kernel<D, Q8><<<(unsigned)(g.B * g.Hq * g.N), 128, 0, stream>>>(
-        q, kd, vd, a.n_nodes, a.k_cache, a.v_cache, ks, vs, a.kv_len, xs, tau, anc, depth, out, g, e_pow, sm2);
-    return cudaGetLastError();
+        a.kv_len, a.n_nodes, w.xs, w.anc, w.depth, w.tau, w.bits, w.tick, w.list, w.count, w.offs, w.plan, out, w.hdr, g, alpha,
+        nctas, kTreePer);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_tree_attn(a, w, g, e_pow, sm2, nctas, kTreePer, stream);
 }
 
 cudaError_t launch_tree(const TreeArgs& a, const TreeGeom& g, char* ws, float alpha, float coarse_scale, cudaStream_t stream) {

@@ -1,0 +1,50 @@
+// tree.cuh -- what the kernels of a drafted-tree decode step share (tree.cu, tree_tc.cu).
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace dash {
+
+constexpr int kTreeOpen = -1, kTreeDraft = -2;   // list entries behind the past blocks
+
+// The workspace's regions.
+struct TreeWork {
+    WsHeader* hdr;
+    float *xs, *tau;                     // scores [rows][cap], thresholds
+    unsigned long long* anc;             // [B][N] ancestors and self (0: an invalid node)
+    int* depth;                          // [B][N]
+    unsigned* bits;                      // [tile][nbw] selected blocks
+    int *tick, *list, *count, *offs, *plan;
+    float* part;                         // [CTA + tile][128][D + 2]
+};
+
+inline TreeWork tree_work(const TreeGeom& g, char* ws) {
+    TreeWork w;
+    w.hdr = reinterpret_cast<WsHeader*>(ws);
+    w.xs = reinterpret_cast<float*>(ws + g.off_x);
+    w.tau = reinterpret_cast<float*>(ws + g.off_tau);
+    w.anc = reinterpret_cast<unsigned long long*>(ws + g.off_anc);
+    w.depth = reinterpret_cast<int*>(ws + g.off_depth);
+    w.bits = reinterpret_cast<unsigned*>(ws + g.off_bits);
+    w.tick = reinterpret_cast<int*>(ws + g.off_tick);
+    w.list = reinterpret_cast<int*>(ws + g.off_list);
+    w.count = reinterpret_cast<int*>(ws + g.off_count);
+    w.offs = reinterpret_cast<int*>(ws + g.off_offs);
+    w.plan = reinterpret_cast<int*>(ws + g.off_plan);
+    w.part = reinterpret_cast<float*>(ws + g.off_part);
+    return w;
+}
+
+// Whether the sequence's length is valid, and how many of its nodes are computed.
+__device__ __forceinline__ bool tree_live(const int* kv_len, const int* n_nodes, const TreeGeom& g, int b, int* L, int* nodes) {
+    *L = kv_len[b];
+    *nodes = n_nodes ? max(0, min(n_nodes[b], g.N)) : g.N;
+    return *L >= 0 && *L <= g.Tmax && *nodes > 0;
+}
+
+// attention over the tiles' lists on nctas CTAs (at least `per` entries each), and the merge
+cudaError_t launch_tree_attn(const TreeArgs& a, const TreeWork& w, const TreeGeom& g, float e_pow, float sm2, int nctas,
+                             int per, cudaStream_t stream);
+
+}  // namespace dash

@@ -1,0 +1,678 @@
+// tree_tc.cu -- attention of a drafted-tree decode step on tcgen05, split over the concatenated
+// lists of the tiles (tree.cu: what a list holds).
+//
+// A tile is up to 128 rows (heads x nodes) of one KV group and the M rows of both products:
+// S = Q K^T (N = 64 keys) into TMEM, softmax weights P in bf16 through shared memory, O += P V
+// and the row sums L += P 1 in TMEM.  The tensor core does 128 rows at the price of one, so
+// rows that a tile lacks cost no time; what bounds the kernel is the K/V stream (each list
+// entry's 64 rows once per tile) and, per step, one row's chain S -> weights -> P.
+//
+// Work split as in decode_tc.cu: the lists laid end to end hold U entries, CTA c of n takes
+// entries [U c / n, U (c + 1) / n); a tile inside one CTA is finished there, the others leave
+// (max, sum, output) per row in slot CTA + tile for tree_combine_kernel.
+//
+// Roles (warps): 0 - 7 softmax, two groups of 128 threads (one per row) that take the steps
+// alternately, each with its own S, P buffers, O, row sum and maximum, merged at the end of a
+// segment; 8 K producer; 9 issuer of S; 10 issuer of P V; 11 V producer.  Counters of rings and
+// barriers run over the CTA's whole range; only the Q tile and the accumulators belong to a
+// segment.  The value rows that no row may attend (the open block's behind the sequence, the
+// draft's behind its nodes) are overwritten with zeros before the product: weight 0 times
+// whatever they hold would not be 0 if that were NaN.
+// 8-bit cache: warp 8 streams codes and scale bytes with bulk copies into a ring of their own,
+// and warps 12 - 15 turn them into the bf16 operand tiles (exact: cache8.cuh) or load the
+// draft's bf16 rows.
+// Every wait is bounded; a CTA that gives up sets a status bit.
+#include "cache8.cuh"
+#include "kernels.h"
+#include "select.cuh"
+#include "sm100.cuh"
+#include "tree.cuh"
+
+namespace dash {
+
+constexpr int kTtK = 2, kTtV = 2;      // operand tile rings of the 8-bit variant
+constexpr int kTtPBuf = 2;             // P buffers per group
+constexpr int kTtRaw = 3;              // 8-bit ring
+constexpr float kTtLazy = 8.0f;        // log2 units a maximum may grow before O is rescaled
+
+template <int D, bool Q8>
+struct TtLayout {
+    static constexpr int kKS = Q8 ? kTtK : 3, kVS = Q8 ? kTtV : 3;
+    static constexpr uint32_t kHalf = 64 * 128;                 // 64 rows x 64 bf16
+    static constexpr uint32_t kTile = (D / 64) * kHalf;         // K or V of one entry
+    static constexpr uint32_t kQHalf = 128 * 128;
+    static constexpr uint32_t kP = 128 * 128;
+    static constexpr uint32_t kRawKV = 64 * D;                  // codes of K or V of one entry
+    static constexpr uint32_t kRaw = 2 * kRawKV + 128;          // and the scale bytes
+    static constexpr uint32_t off_q = 0;
+    static constexpr uint32_t off_k = (D / 64) * kQHalf;
+    static constexpr uint32_t off_v = off_k + kKS * kTile;
+    static constexpr uint32_t off_p = off_v + kVS * kTile;
+    static constexpr uint32_t off_ones = off_p + 2 * kTtPBuf * kP;
+    static constexpr uint32_t off_raw = off_ones + 2048;
+    static constexpr uint32_t bytes = off_raw + (Q8 ? kTtRaw * kRaw : 0) + 1024;
+    static_assert(bytes + 4096 <= 227 * 1024, "shared memory of one CTA per SM");
+    // TMEM columns: S of group g at 64 g, O at 128 + D g, row sums at 384 + 16 g
+    static constexpr uint32_t colO = 128, colL = 384;
+};
+
+// One 32-bit word of codes as four bf16, scaled: the code's exponent and mantissa bits moved to
+// bf16's place read as code 2^-120 (subnormals too), so two exact multiplications by powers of
+// two give code 2^(s - 127).
+__device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t w, __nv_bfloat162 f, uint32_t* lo, uint32_t* hi) {
+    const __nv_bfloat162 up = __floats2bfloat162_rn(0x1p120f, 0x1p120f);
+    const uint32_t e = __byte_perm(w, 0u, 0x1404), o = __byte_perm(w, 0u, 0x3424);   // codes 0, 1 and 2, 3 in the high bytes
+    const uint32_t a = (e & 0x80008000u) | ((e >> 4) & 0x07f007f0u), b = (o & 0x80008000u) | ((o >> 4) & 0x07f007f0u);
+    const __nv_bfloat162 x = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), up), f);
+    const __nv_bfloat162 y = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), up), f);
+    *lo = *reinterpret_cast<const uint32_t*>(&x);
+    *hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
+tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ CUtensorMap tm_kd, const __grid_constant__ CUtensorMap tm_vd, TreeArgs a,
+                 TreeWork w, TreeGeom g, float e_pow, float sm2, int per) {
+    using L = TtLayout<D, Q8>;
+    using namespace sm100;
+    constexpr int KS = L::kKS, VS = L::kVS;
+    enum : int { B_Q = 0, B_KF = 1, B_KE = B_KF + KS, B_VF = B_KE + KS, B_VE = B_VF + VS, B_SF = B_VE + VS, B_SE = B_SF + 2,
+                 B_PF = B_SE + 2, B_PD = B_PF + 2 * kTtPBuf, B_RF = B_PD + 2 * kTtPBuf, B_RE = B_RF + kTtRaw,
+                 B_VT = B_RE + kTtRaw, B_DR = B_VT + 1, B_COUNT = B_DR + 2 };
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[B_COUNT];
+    __shared__ uint32_t tmem_sh;
+    __shared__ int abort_sh;
+    __shared__ float m_sh[2][kTreeRows];
+    const long long U = w.offs[g.tiles];
+    const int nC = split_ctas(U, (int)gridDim.x, per), cta = blockIdx.x;
+    if (cta >= nC) return;
+    const int r_lo = (int)(U * cta / nC), r_hi = (int)(U * (cta + 1) / nC);
+    const int tile_first = w.plan[cta];
+
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const base_ptr = smem_raw + (base - raw);
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const auto* q = static_cast<const __nv_bfloat16*>(a.q);
+    if (tid == 0) {
+        abort_sh = 0;
+        const int conv = Q8 ? 128 : 1;                          // who fills an operand tile
+        mbar_init(bar(B_Q), 256);
+        for (int i = 0; i < KS; ++i) { mbar_init(bar(B_KF + i), conv); mbar_init(bar(B_KE + i), 1); }
+        for (int i = 0; i < VS; ++i) { mbar_init(bar(B_VF + i), conv); mbar_init(bar(B_VE + i), 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(bar(B_SF + i), 1); mbar_init(bar(B_SE + i), 128); mbar_init(bar(B_DR + i), 1); }
+        for (int i = 0; i < 2 * kTtPBuf; ++i) { mbar_init(bar(B_PF + i), 128); mbar_init(bar(B_PD + i), 1); }
+        for (int i = 0; i < kTtRaw; ++i) { mbar_init(bar(B_RF + i), 1); mbar_init(bar(B_RE + i), 128); }
+        mbar_init(bar(B_VT), 1);
+        fence_mbar_init();
+    }
+    if (tid < 128) reinterpret_cast<uint4*>(base_ptr + L::off_ones)[tid] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    fence_proxy_async_smem();
+    if (warp == 0) {
+        tmem_alloc(smem_u32(&tmem_sh), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_sh;
+    volatile int* abort_flag = &abort_sh;
+    auto k_addr = [&](int st) { return base + L::off_k + (uint32_t)st * L::kTile; };
+    auto v_addr = [&](int st) { return base + L::off_v + (uint32_t)st * L::kTile; };
+
+    // calls body(tile, first entry, entries, step count before) for every segment of the range
+    auto segments = [&](auto&& body) {
+        int gs = 0;
+        for (int tile = tile_first, pos = r_lo; pos < r_hi; ++tile) {
+            const int o0 = w.offs[tile], o1 = w.offs[tile + 1];
+            if (o1 <= pos) continue;
+            const int n = min(r_hi, o1) - pos;
+            body(tile, pos - o0, n, gs);
+            pos += n;
+            gs += n;
+        }
+    };
+
+    if (warp == 8) {
+        // ------------------------------------------------------------ K producer / 8-bit stream
+        if (lane == 0) {
+            bool ok = true;
+            int armed = 0;                                       // steps loaded
+            if constexpr (!Q8) { prefetch_tmap(&tm_k); prefetch_tmap(&tm_kd); }
+            segments([&](int tile, int e0, int n, int gs) {
+                const int bg = tile / g.tiles_bg;
+                const int F = a.kv_len[bg / g.Hkv] / kBlock;
+                for (int s = 0; ok && s < n; ++s) {
+                    const int j = w.list[(size_t)tile * g.lcap + e0 + s];
+                    if constexpr (Q8) {
+                        if (j == kTreeDraft) continue;           // loaded by the converters
+                        const int st = armed % kTtRaw;
+                        if (armed >= kTtRaw && !mbar_wait(bar(B_RE + st), ((armed / kTtRaw) - 1) & 1, abort_flag)) { ok = false; break; }
+                        const size_t row = (size_t)bg * g.Tmax + (size_t)(j == kTreeOpen ? F : j) * kBlock;
+                        const uint32_t dst = base + L::off_raw + (uint32_t)st * L::kRaw, bf = bar(B_RF + st);
+                        mbar_arrive_expect_tx(bf, L::kRaw);
+                        bulk_load_1d(dst, static_cast<const uint8_t*>(a.k_cache) + row * D, L::kRawKV, bf);
+                        bulk_load_1d(dst + L::kRawKV, static_cast<const uint8_t*>(a.v_cache) + row * D, L::kRawKV, bf);
+                        bulk_load_1d(dst + 2 * L::kRawKV, static_cast<const uint8_t*>(a.k_scale) + row, 64, bf);
+                        bulk_load_1d(dst + 2 * L::kRawKV + 64, static_cast<const uint8_t*>(a.v_scale) + row, 64, bf);
+                    } else {
+                        const int st = (gs + s) % KS;
+                        if (gs + s >= KS && !mbar_wait(bar(B_KE + st), (((gs + s) / KS) - 1) & 1, abort_flag)) { ok = false; break; }
+                        mbar_arrive_expect_tx(bar(B_KF + st), L::kTile);
+                        const CUtensorMap* tm = j == kTreeDraft ? &tm_kd : &tm_k;
+                        const int row = j == kTreeDraft ? bg * g.N : bg * g.Tmax + (j == kTreeOpen ? F : j) * kBlock;
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h) tma_load_2d(k_addr(st) + h * L::kHalf, tm, h * 64, row, bar(B_KF + st));
+                    }
+                    ++armed;
+                }
+            });
+            if (!ok) {
+                // every load this thread started lands before the CTA exits
+                constexpr int NS = Q8 ? kTtRaw : KS;
+                volatile int dummy = 0;
+                for (int st = 0; st < NS; ++st) {
+                    if (armed <= st) continue;
+                    const int last = armed - 1 - ((armed - 1 - st) % NS);
+                    dummy = 0;
+                    mbar_wait(bar((Q8 ? (int)B_RF : (int)B_KF) + st), (last / NS) & 1, &dummy);
+                }
+            }
+        }
+    } else if (warp == 11) {
+        // ------------------------------------------------------------ V producer (bf16 cache)
+        if constexpr (!Q8) {
+            bool ok = true;
+            int special = 0, last_st[VS];
+#pragma unroll
+            for (int i = 0; i < VS; ++i) last_st[i] = -1;
+            if (lane == 0) { prefetch_tmap(&tm_v); prefetch_tmap(&tm_vd); }
+            segments([&](int tile, int e0, int n, int gs) {
+                const int bg = tile / g.tiles_bg, b = bg / g.Hkv;
+                int len, nodes;
+                tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes);
+                const int F = len / kBlock;
+                for (int s = 0; ok && s < n; ++s) {
+                    const int j = w.list[(size_t)tile * g.lcap + e0 + s];
+                    const int st = (gs + s) % VS;
+                    bool got = gs + s < VS || mbar_wait(bar(B_VE + st), (((gs + s) / VS) - 1) & 1, abort_flag);
+                    if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                    const CUtensorMap* tm = j == kTreeDraft ? &tm_vd : &tm_v;
+                    const int row = j == kTreeDraft ? bg * g.N : bg * g.Tmax + (j == kTreeOpen ? F : j) * kBlock;
+                    const int bf = j < 0 ? (int)B_VT : (int)B_VF + st;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar(bf), L::kTile);
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h) tma_load_2d(v_addr(st) + h * L::kHalf, tm, h * 64, row, bar(bf));
+                    }
+                    if (j < 0) {
+                        got = mbar_wait(bar(B_VT), special & 1, abort_flag);
+                        ++special;
+                        if (!__all_sync(0xffffffffu, got)) {
+                            // the special load itself is still to land
+                            volatile int dummy = 0;
+                            if (!got) mbar_wait(bar(B_VT), (special - 1) & 1, &dummy);
+                            ok = false;
+                            break;
+                        }
+                        const int lim = j == kTreeDraft ? nodes : len % kBlock;
+                        for (int i = lane; i < (kBlock - lim) * (D / 8); i += 32) {
+                            const int r = lim + i / (D / 8), c = i % (D / 8);
+                            *reinterpret_cast<uint4*>(base_ptr + L::off_v + st * L::kTile + (c >> 3) * L::kHalf + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(B_VF + st));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < VS; ++i)
+                            if (i == st) last_st[i] = gs + s;
+                    }
+                }
+            });
+            if (!ok && lane == 0) {
+                volatile int dummy = 0;
+#pragma unroll
+                for (int i = 0; i < VS; ++i)
+                    if (last_st[i] >= 0) { dummy = 0; mbar_wait(bar(B_VF + i), (last_st[i] / VS) & 1, &dummy); }
+            }
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ S issuer
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16(128, 64, false);
+            bool ok = true;
+            int seg = 0;
+            segments([&](int, int, int n, int gs0) {
+                if (ok && !mbar_wait(bar(B_Q), seg & 1, abort_flag)) ok = false;
+                ++seg;
+                for (int s = 0; ok && s < n; ++s) {
+                    const int gs = gs0 + s, st = gs % KS, sb = gs & 1, i2 = gs >> 1;
+                    if (!mbar_wait(bar(B_KF + st), (gs / KS) & 1, abort_flag)) { ok = false; break; }
+                    if (i2 >= 1 && !mbar_wait(bar(B_SE + sb), (i2 - 1) & 1, abort_flag)) { ok = false; break; }
+                    // a group that sees this S may write its P buffer: the buffer's last product has landed
+                    if (i2 >= kTtPBuf && !mbar_wait(bar(B_PD + kTtPBuf * sb + i2 % kTtPBuf), ((i2 - kTtPBuf) / kTtPBuf) & 1, abort_flag)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t da = smem_desc_sw128(base + L::off_q + (kk >> 2) * L::kQHalf + (kk & 3) * 32, 16, 1024);
+                        const uint64_t db = smem_desc_sw128(k_addr(st) + (kk >> 2) * L::kHalf + (kk & 3) * 32, 16, 1024);
+                        mma_bf16_ss(tmem + sb * 64, da, db, idesc, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit(bar(B_SF + sb));
+                    mma_commit(bar(B_KE + st));
+                }
+            });
+            if (!ok) {
+                mma_commit(bar(B_DR));
+                volatile int dummy = 0;
+                mbar_wait(bar(B_DR), 0, &dummy);
+            }
+        }
+    } else if (warp == 10) {
+        // ------------------------------------------------------------ PV issuer
+        if (lane == 0) {
+            const uint32_t idesc_v = idesc_bf16(128, D, true), idesc_l = idesc_bf16(128, 16, false);
+            bool ok = true;
+            segments([&](int, int, int n, int gs0) {
+                for (int s = 0; ok && s < n; ++s) {
+                    const int gs = gs0 + s, st = gs % VS, gp = gs & 1, i2 = gs >> 1, pb = kTtPBuf * gp + i2 % kTtPBuf;
+                    if (!mbar_wait(bar(B_PF + pb), (i2 / kTtPBuf) & 1, abort_flag)) { ok = false; break; }
+                    if (!mbar_wait(bar(B_VF + st), (gs / VS) & 1, abort_flag)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t acc = s >= 2 ? 1u : 0u;       // a group's first step of the segment overwrites
+                    const uint32_t pa = base + L::off_p + pb * L::kP;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t da = smem_desc_sw128(pa + kk * 32, 16, 1024);
+                        const uint64_t dv = smem_desc_sw128(v_addr(st) + kk * 2048, L::kHalf, 1024);
+                        mma_bf16_ss(tmem + L::colO + gp * D, da, dv, idesc_v, (acc || kk > 0) ? 1u : 0u);
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t da = smem_desc_sw128(pa + kk * 32, 16, 1024);
+                        const uint64_t d1 = smem_desc_sw128(base + L::off_ones + kk * 32, 16, 1024);
+                        mma_bf16_ss(tmem + L::colL + gp * 16, da, d1, idesc_l, (acc || kk > 0) ? 1u : 0u);
+                    }
+                    mma_commit(bar(B_PD + pb));
+                    mma_commit(bar(B_VE + st));
+                }
+            });
+            if (!ok) {
+                mma_commit(bar(B_DR + 1));
+                volatile int dummy = 0;
+                mbar_wait(bar(B_DR + 1), 0, &dummy);
+            }
+        }
+    } else if (warp >= 12) {
+        // ------------------------------------------------------------ converters (8-bit cache)
+        if constexpr (Q8) {
+            constexpr int CH = D / 16;                           // 16-code chunks per row
+            const int ct = tid - 384;
+            bool ok = true;
+            int rs = 0;                                          // raw stages taken
+            segments([&](int tile, int e0, int n, int gs0) {
+                const int bg = tile / g.tiles_bg, b = bg / g.Hkv;
+                int len, nodes;
+                tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes);
+                for (int s = 0; s < n; ++s) {
+                    const int gs = gs0 + s;
+                    const int j = w.list[(size_t)tile * g.lcap + e0 + s];
+                    const bool draft = j == kTreeDraft;
+                    const int lim = draft ? nodes : j == kTreeOpen ? len % kBlock : kBlock;   // rows that are there
+                    const int rst = rs % kTtRaw;
+                    if (!draft) {
+                        ok = ok && mbar_wait(bar(B_RF + rst), (rs / kTtRaw) & 1, abort_flag);
+                        ++rs;
+                    }
+                    const uint8_t* rp = base_ptr + L::off_raw + rst * L::kRaw;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        constexpr int NS = kTtK;
+                        const int st = gs % NS;
+                        ok = ok && (gs < NS || mbar_wait(bar((kv ? (int)B_VE : (int)B_KE) + st), ((gs / NS) - 1) & 1, abort_flag));
+                        if (ok) {
+                            uint8_t* dst = base_ptr + (kv ? L::off_v : L::off_k) + st * L::kTile;
+                            const auto* dr = static_cast<const __nv_bfloat16*>(kv ? a.v_draft : a.k_draft) + (size_t)bg * g.N * D;
+#pragma unroll
+                            for (int it = 0; it < kBlock * CH / 128; ++it) {
+                                const int idx = it * 128 + ct, r = idx / CH, c = idx % CH;
+                                uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+                                if (r < lim) {
+                                    if (draft) {
+                                        const uint4* p = reinterpret_cast<const uint4*>(dr + (size_t)r * D) + c * 2;
+                                        lo = __ldg(p);
+                                        hi = __ldg(p + 1);
+                                    } else {
+                                        const uint4 x = *reinterpret_cast<const uint4*>(rp + kv * L::kRawKV + idx * 16);
+                                        const float fs = scale_value(rp[2 * L::kRawKV + kv * 64 + r]);
+                                        const __nv_bfloat162 f = __floats2bfloat162_rn(fs, fs);
+                                        e4m3x4_to_bf16x4(x.x, f, &lo.x, &lo.y);
+                                        e4m3x4_to_bf16x4(x.y, f, &lo.z, &lo.w);
+                                        e4m3x4_to_bf16x4(x.z, f, &hi.x, &hi.y);
+                                        e4m3x4_to_bf16x4(x.w, f, &hi.z, &hi.w);
+                                    }
+                                }
+                                // chunks 2 c and 2 c + 1 of the row's half; the upper half's lanes store the
+                                // odd chunk first, so the lanes of a phase fall in distinct banks
+                                uint8_t* row = dst + (c >> 2) * L::kHalf + r * 128;
+                                const int c0 = (c & 3) * 2, sw = c >> 2;
+                                *reinterpret_cast<uint4*>(row + (((c0 + sw) ^ (r & 7)) << 4)) = sw ? hi : lo;
+                                *reinterpret_cast<uint4*>(row + (((c0 + 1 - sw) ^ (r & 7)) << 4)) = sw ? lo : hi;
+                            }
+                            fence_proxy_async_smem();
+                            mbar_arrive(bar((kv ? (int)B_VF : (int)B_KF) + st));
+                        }
+                    }
+                    if (!draft && ok) mbar_arrive(bar(B_RE + rst));
+                }
+            });
+        }
+    } else {
+        // ------------------------------------------------------------ softmax groups
+        const int grp = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t s_col = grp * 64, o_col = L::colO + grp * D, l_col = L::colL + grp * 16;
+        uint8_t* const prow0 = base_ptr + L::off_p + kTtPBuf * grp * L::kP + (r >> 3) * 1024 + (r & 7) * 128;
+        bool ok = true;
+        auto wwait = [&](uint32_t bar_addr, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, abort_flag));
+        };
+        segments([&](int tile, int e0, int n, int gs0) {
+            const int bg = tile / g.tiles_bg, b = bg / g.Hkv, row_g = (tile % g.tiles_bg) * kTreeRows + r;
+            const bool in_tile = row_g < g.R;
+            const size_t row = (size_t)bg * g.R + row_g;
+            // Q tile: two threads per row
+            {
+                const int half = grp;                            // this group's dims of the row
+                const uint4* src = reinterpret_cast<const uint4*>(q + row * D) + half * (D / 16);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    const uint4 v = in_tile ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                    const int cc = half * (D / 16) + c;
+                    *reinterpret_cast<uint4*>(base_ptr + L::off_q + (cc >> 3) * L::kQHalf + r * 128 + (((cc & 7) ^ (r & 7)) << 4)) = v;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(bar(B_Q));
+            }
+            int len, nodes;
+            tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes);
+            const int F = len / kBlock, rem = len % kBlock, node = in_tile ? row_g % g.N : 0;
+            const size_t bn = (size_t)b * g.N;
+            const unsigned long long anc = in_tile && node < nodes ? w.anc[bn + node] : 0ull;
+            const bool valid = anc != 0ull;
+            const bool warp_live = __any_sync(0xffffffffu, valid);
+            const float tau_r = valid ? w.tau[row] : __int_as_float(0x7fc00000);
+            const float* xr = w.xs + row * g.cap;
+            const bool crossed = valid && rem + w.depth[bn + node] >= kBlock;
+            const float xF = crossed ? xr[F] : 0.f;
+            // log2 prior of the open block's keys: 1 while it is the own block
+            const float lpo = !crossed ? 0.f : (xF > tau_r ? e_pow * __log2f(xF - tau_r) : -INFINITY);
+            auto entry = [&](int s) { return s < n ? w.list[(size_t)tile * g.lcap + e0 + s] : kTreeDraft; };
+            auto xval = [&](int j) { return valid && j >= 0 ? __ldcg(xr + j) : 0.f; };
+            const int s0 = (gs0 & 1) == grp ? 0 : 1;
+            int j0 = entry(s0), j1 = entry(s0 + 2);
+            float x0 = xval(j0);
+            float m_run = -INFINITY;
+            for (int s = s0; s < n; s += 2) {
+                const int gs = gs0 + s, i2 = gs >> 1, pb = i2 % kTtPBuf;
+                const float x1 = xval(j1);                       // the next steps' values, on their way early
+                const int j2 = entry(s + 4);
+                const int j = j0;
+                const float x = x0;
+                j0 = j1; j1 = j2; x0 = x1;
+                if (!(ok && wwait(bar(B_SF + grp), i2 & 1))) { ok = false; continue; }
+                if (!warp_live) {
+                    // no row of this warp is used; its lanes of S, P and O hold whatever they hold
+                    mbar_arrive(bar(B_SE + grp));
+                    mbar_arrive(bar(B_PF + kTtPBuf * grp + pb));
+                    continue;
+                }
+                tc_fence_after();
+                uint32_t sr[64];
+                tmem_ld<64>(lane_addr + s_col, sr);
+                tmem_wait_ld();
+                tc_fence_before();
+                mbar_arrive(bar(B_SE + grp));
+                float scale = sm2, lp2;
+                if (j >= 0) {
+                    lp2 = valid && x > tau_r ? e_pow * __log2f(x - tau_r) : -INFINITY;
+                } else if (j == kTreeOpen) {
+                    lp2 = valid ? lpo : -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        if (i >= rem) sr[i] = __float_as_uint(-INFINITY);
+                } else {
+                    // the draft: ancestors and self; those in a completed open block carry its prior
+                    unsigned long long low = 0ull;
+                    if (crossed)
+                        for (int i = 0; i < nodes; ++i)
+                            if (rem + w.depth[bn + i] < kBlock) low |= 1ull << i;
+                    lp2 = valid ? 0.f : -INFINITY;
+                    scale = 1.f;
+                    const uint32_t a0 = (uint32_t)anc, a1 = (uint32_t)(anc >> 32), l0 = (uint32_t)low, l1 = (uint32_t)(low >> 32);
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) {
+                        const uint32_t am = i < 32 ? a0 : a1, lm = i < 32 ? l0 : l1;
+                        float v = __uint_as_float(sr[i]) * sm2;
+                        if ((lm >> (i & 31)) & 1u) v = lpo == -INFINITY ? -INFINITY : v + lpo;
+                        if (!((am >> (i & 31)) & 1u)) v = -INFINITY;
+                        sr[i] = __float_as_uint(v);
+                    }
+                }
+                float mx = -INFINITY;
+                if (lp2 > -INFINITY) {
+                    float m4[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m4[i] = fmaxf(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]));
+#pragma unroll
+                    for (int i = 4; i < 32; ++i) m4[i & 3] = max3(m4[i & 3], __uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]));
+                    mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), scale, lp2);
+                }
+                const bool active = mx > -INFINITY;
+                float factor = 1.f;
+                bool resc = false;
+                if (active) {
+                    if (m_run == -INFINITY) m_run = mx;
+                    else if (mx > m_run + kTtLazy) { factor = exp2f(m_run - mx); m_run = mx; resc = true; }
+                }
+                uint8_t* const prow = prow0 + pb * L::kP;
+                const float c0 = lp2 - m_run;
+                const uint64_t sc2 = f2_pack(__float_as_uint(scale), __float_as_uint(scale));
+                const uint64_t c2 = f2_pack(__float_as_uint(c0), __float_as_uint(c0));
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t pk[4] = {0u, 0u, 0u, 0u};
+                    if (active) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float v0, v1;
+                            f2_unpack(f2_fma(f2_pack(sr[c * 8 + 2 * i], sr[c * 8 + 2 * i + 1]), sc2, c2), v0, v1);
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(fast_exp2(v0), fast_exp2(v1));
+                            pk[i] = *reinterpret_cast<const uint32_t*>(&h2);
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+                if (__any_sync(0xffffffffu, resc)) {
+                    // the group's previous product has landed before O and the row sums are rescaled
+                    if (!wwait(bar(B_PD + kTtPBuf * grp + (i2 - 1) % kTtPBuf), ((i2 - 1) / kTtPBuf) & 1)) { ok = false; continue; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(lane_addr + o_col + c * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+                        tmem_st32(lane_addr + o_col + c * 32, o);
+                    }
+                    uint32_t o[16];
+                    tmem_ld16(lane_addr + l_col, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+                    tmem_st16(lane_addr + l_col, o);
+                    tmem_wait_st();
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(bar(B_PF + kTtPBuf * grp + pb));
+            }
+            // ---- the two groups' states: (max, sum, output) of every row
+            m_sh[grp][r] = m_run;
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            const int gl = gs0 + n - 1;                          // last step; the other group's last is before it
+            const bool both = n >= 2;
+            bool done = ok;
+            {
+                const int i2 = gl >> 1, p = kTtPBuf * (gl & 1) + i2 % kTtPBuf;
+                done = done && wwait(bar(B_PD + p), (i2 / kTtPBuf) & 1);
+            }
+            if (both) {
+                const int i2 = (gl - 1) >> 1, p = kTtPBuf * ((gl - 1) & 1) + i2 % kTtPBuf;
+                done = done && wwait(bar(B_PD + p), (i2 / kTtPBuf) & 1);
+            }
+            if (done && warp_live) {
+                tc_fence_after();
+                const bool has0 = both || (gl & 1) == 0, has1 = both || (gl & 1) == 1;
+                const float m0 = has0 ? m_sh[0][r] : -INFINITY, m1 = has1 ? m_sh[1][r] : -INFINITY;
+                const float M = fmaxf(m0, m1);
+                const float w0 = m0 == -INFINITY ? 0.f : exp2f(m0 - M), w1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
+                const float l0 = __uint_as_float(tmem_ld1(lane_addr + L::colL)), l1 = __uint_as_float(tmem_ld1(lane_addr + L::colL + 16));
+                tmem_wait_ld();
+                const float den = (w0 > 0.f ? l0 * w0 : 0.f) + (w1 > 0.f ? l1 * w1 : 0.f);
+                const int o0 = w.offs[tile], o1 = w.offs[tile + 1];
+                const bool direct = dt_cta_of(o0, U, nC) == dt_cta_of(o1 - 1, U, nC);
+                float* pr = w.part + (((size_t)cta + tile) * kTreeRows + r) * (D + 2);
+                if (!direct && valid && grp == 0) { pr[0] = M; pr[1] = den; }
+                const float inv = direct ? 1.0f / den : 1.0f;
+                auto* out = static_cast<__nv_bfloat16*>(a.out) + row * D;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    const int col = grp * (D / 2) + c * 32;      // the groups share the row's columns
+                    uint32_t p0[32], p1[32];
+                    tmem_ld32(lane_addr + L::colO + col, p0);
+                    tmem_ld32(lane_addr + L::colO + D + col, p1);
+                    tmem_wait_ld();
+                    if (valid) {
+                        float f[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            float v = w0 > 0.f ? __uint_as_float(p0[i]) * w0 : 0.f;
+                            if (w1 > 0.f) v = fmaf(__uint_as_float(p1[i]), w1, v);
+                            f[i] = v * inv;
+                        }
+                        if (direct) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t pk[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const __nv_bfloat162 h2 = __floats2bfloat162_rn(f[8 * i + 2 * k], f[8 * i + 2 * k + 1]);
+                                    pk[k] = *reinterpret_cast<const uint32_t*>(&h2);
+                                }
+                                *reinterpret_cast<uint4*>(out + col + 8 * i) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) *reinterpret_cast<float2*>(pr + 2 + col + 2 * i) = make_float2(f[2 * i], f[2 * i + 1]);
+                        }
+                    }
+                }
+            }
+            // Q, O and the maxima are free for the next segment
+            tc_fence_before();
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+        });
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (tid == 0 && abort_sh) atomicOr(&w.hdr->status, kStWaitTimeout);
+}
+
+// One warp per row of a tile that several CTAs share: merges their partials.
+template <int D>
+__global__ void __launch_bounds__(256)
+tree_combine_kernel(TreeArgs a, TreeWork w, TreeGeom g, int nctas, int per) {
+    constexpr int kPerTile = kTreeRows / 8, DPL = D / 32;
+    const int tile = blockIdx.x / kPerTile, r = (blockIdx.x % kPerTile) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int bg = tile / g.tiles_bg, b = bg / g.Hkv, row_g = (tile % g.tiles_bg) * kTreeRows + r;
+    if (row_g >= g.R) return;
+    const long long U = w.offs[g.tiles];
+    const int o0 = w.offs[tile], o1 = w.offs[tile + 1];
+    if (o1 == o0) return;
+    const int nC = split_ctas(U, nctas, per);
+    const int c0 = dt_cta_of(o0, U, nC), c1 = dt_cta_of(o1 - 1, U, nC);
+    if (c0 == c1) return;
+    int len, nodes;
+    if (!tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes)) return;
+    const int node = row_g % g.N;
+    if (node >= nodes || !w.anc[(size_t)b * g.N + node]) return;
+    const float* p = w.part + (((size_t)c0 + tile) * kTreeRows + r) * (D + 2);
+    const size_t step = (size_t)kTreeRows * (D + 2);
+    const int np = c1 - c0 + 1;
+    float M = -INFINITY;
+    for (int i = lane; i < np; i += 32) M = fmaxf(M, __ldcg(p + i * step));
+    M = warp_max(M);
+    float num[DPL], den = 0.f;
+#pragma unroll
+    for (int d = 0; d < DPL; ++d) num[d] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < np; ++i) {
+        const float* pi = p + i * step;
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(pi));
+        float v[DPL];
+#pragma unroll
+        for (int d = 0; d < DPL / 2; ++d) {
+            const float2 t = __ldcg(reinterpret_cast<const float2*>(pi + 2 + lane * DPL + 2 * d));
+            v[2 * d] = t.x; v[2 * d + 1] = t.y;
+        }
+        const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+        den = fmaf(ml.y, wt, den);
+#pragma unroll
+        for (int d = 0; d < DPL; ++d) num[d] = fmaf(v[d], wt, num[d]);
+    }
+    const float inv = 1.0f / den;
+    auto* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)bg * g.R + row_g) * D + lane * DPL;
+#pragma unroll
+    for (int d = 0; d < DPL / 2; ++d) *reinterpret_cast<__nv_bfloat162*>(out + 2 * d) = __floats2bfloat162_rn(num[2 * d] * inv, num[2 * d + 1] * inv);
+}
+
+template <int D, bool Q8>
+static cudaError_t launch_t(const TreeArgs& a, const TreeWork& w, const TreeGeom& g, float e_pow, float sm2, int nctas,
+                            int per, cudaStream_t stream) {
+    CUtensorMap tk = {}, tv = {}, tkd = {}, tvd = {};
+    if constexpr (!Q8) {
+        const unsigned long long rows = (unsigned long long)g.B * g.Hkv * g.Tmax, drows = (unsigned long long)g.B * g.Hkv * g.N;
+        if (!make_tmap_bf16(&tk, a.k_cache, rows, D, kBlock) || !make_tmap_bf16(&tv, a.v_cache, rows, D, kBlock) ||
+            !make_tmap_bf16(&tkd, a.k_draft, drows, D, kBlock) || !make_tmap_bf16(&tvd, a.v_draft, drows, D, kBlock))
+            return cudaErrorInvalidValue;
+    }
+    const int sm = (int)TtLayout<D, Q8>::bytes;
+    cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+    if (e != cudaSuccess) return e;
+    tree_attn_kernel<D, Q8><<<nctas, Q8 ? 512 : 384, sm, stream>>>(tk, tv, tkd, tvd, a, w, g, e_pow, sm2, per);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    tree_combine_kernel<D><<<(unsigned)g.tiles * (kTreeRows / 8), 256, 0, stream>>>(a, w, g, nctas, per);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_tree_attn(const TreeArgs& a, const TreeWork& w, const TreeGeom& g, float e_pow, float sm2, int nctas,
+                             int per, cudaStream_t stream) {
+    if (nctas < 1 || nctas > kDecodeMaxCtas) return cudaErrorInvalidValue;
+    if (g.d == 128) return a.k_scale ? launch_t<128, true>(a, w, g, e_pow, sm2, nctas, per, stream)
+                                     : launch_t<128, false>(a, w, g, e_pow, sm2, nctas, per, stream);
+    return a.k_scale ? launch_t<64, true>(a, w, g, e_pow, sm2, nctas, per, stream)
+                     : launch_t<64, false>(a, w, g, e_pow, sm2, nctas, per, stream);
+}
+
+}  // namespace dash
