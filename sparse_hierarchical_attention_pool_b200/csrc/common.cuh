@@ -207,9 +207,9 @@ inline bool make_decode_q8_geom(int B, int Hq, int Hkv, int Tmax, int d, DecodeQ
     g->split = 1;
     while (g->real.G % g->split != 0 || g->real.G / g->split > 8) ++g->split;
     if (!make_decode_geom(B, Hq, Hkv * g->split, Tmax, d, &g->v)) return false;
-    // partials hold two maxima, the sum and the output per head
+    // partials hold two maxima and the sum (16 bytes with padding) and the output per head
     const size_t slots = (size_t)B * Hkv * g->split + kDecodeMaxCtas;
-    g->v.total = align256(g->v.off_part + slots * g->v.G * (d + 3) * sizeof(float));
+    g->v.total = align256(g->v.off_part + slots * g->v.G * (d + 4) * sizeof(float));
     return true;
 }
 
@@ -226,8 +226,8 @@ struct TreeGeom {
     int lcap;                        // list entries per tile: the full blocks, the open one, the tree
     int nbw;                         // 32-bit words of a tile's selection bitmap
     int maxit;
-    size_t off_x, off_tau, off_anc, off_depth, off_bits, off_tick, off_list, off_count, off_offs, off_plan, off_part,
-        total;
+    size_t off_x, off_tau, off_anc, off_depth, off_path, off_bits, off_tick, off_list, off_count, off_offs, off_plan,
+        off_part, total;
 };
 
 inline bool make_tree_geom(int B, int Hq, int Hkv, int N, int Tmax, int d, TreeGeom* g) {
@@ -249,14 +249,15 @@ inline bool make_tree_geom(int B, int Hq, int Hkv, int N, int Tmax, int d, TreeG
     g->off_tau = off;   off = align256(off + rows * sizeof(float));
     g->off_anc = off;   off = align256(off + (size_t)B * N * sizeof(unsigned long long));
     g->off_depth = off; off = align256(off + (size_t)B * N * sizeof(int));
+    g->off_path = off;  off = align256(off + (size_t)B * Hkv * N * d * sizeof(float));
     g->off_bits = off;  off = align256(off + tiles * g->nbw * sizeof(unsigned));
     g->off_tick = off;  off = align256(off + tiles * sizeof(int));
     g->off_list = off;  off = align256(off + tiles * g->lcap * sizeof(int));
     g->off_count = off; off = align256(off + tiles * sizeof(int));
     g->off_offs = off;  off = align256(off + (tiles + 1) * sizeof(int));
     g->off_plan = off;  off = align256(off + (size_t)kDecodeMaxCtas * sizeof(int));
-    // partial (max, sum, output) per row of a (CTA + tile) slot
-    g->off_part = off;  off = align256(off + (tiles + kDecodeMaxCtas) * kTreeRows * (d + 2) * sizeof(float));
+    // partial (max, sum, padding to 16 bytes, output) per row of a (CTA + tile) slot
+    g->off_part = off;  off = align256(off + (tiles + kDecodeMaxCtas) * kTreeRows * (d + 4) * sizeof(float));
     g->total = off;
     return true;
 }
@@ -303,8 +304,11 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, int src_b
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n"
                  :: "r"(smem_u32(dst)), "l"(src), "r"(src_bytes));
 }
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" :: "r"(smem_u32(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::); }
 template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;\n" :: "n"(N)); }
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;\n" :: "n"(N) : "memory"); }
 
 }  // namespace dash

@@ -7,8 +7,8 @@
 // log p as the prior.  Kernels, all launched with shapes known on the host:
 //   1. decode_scores : x[b, h, j] for every head of a KV group, each block summary read once
 //                      for all G heads (a warp streams 16 summaries of one group);
-//   2. decode_select : per (b, kv head): one warp per head solves tau with the row in
-//                      registers, the union of the heads' selected blocks becomes the
+//   2. decode_select : per (b, kv head): one warp per head solves tau with the row in shared
+//                      memory, the union of the heads' selected blocks becomes the
 //                      group's list (own block last), and the last CTA writes the work plan
 //                      of the balanced attention pass;
 //   3. attention     : decode_attn_tc_kernel (decode_tc.cu) for G <= 8, which also merges
@@ -231,10 +231,9 @@ void launch_scores(const __nv_bfloat16* q, const float* ksum, const int* kv_len,
 // ------------------------------------------------------------------ select
 
 // One CTA of 8 warps per (b, kv head).  Warp w solves the thresholds of heads w, w + 8, ...
-// with the row in registers (one warp per head: no cross-warp reduction in a pass).  The
-// heads' selected blocks are OR-ed into a bitmap; every thread then takes bitmap words
-// w, w + 256, ..., a block-wide scan of their popcounts places the words, and each thread
-// writes its words' blocks into the group's list, the own block last.
+// with the row in shared memory (one warp per head: no cross-warp reduction in a pass).  The
+// heads' selected blocks are OR-ed into a bitmap, which becomes the group's list, the own block
+// last.
 constexpr int kSelThreads = 256;
 
 __global__ void __launch_bounds__(kSelThreads)
@@ -242,12 +241,13 @@ decode_select_kernel(const int* __restrict__ kv_len, const float* __restrict__ x
                      float* __restrict__ tau, int* __restrict__ list, int* __restrict__ count,
                      int* __restrict__ done, int* __restrict__ offs, int* __restrict__ plan,
                      __nv_bfloat16* __restrict__ out, WsHeader* __restrict__ hdr, DecodeGeom g,
-                     float alpha, int nctas, int hist_init) {
+                     float alpha, int nctas, int per, int hist_init) {
     constexpr int kWords = kMaxT / kBlock / 32;
     __shared__ HistBins hist[kSelThreads / 32];
-    constexpr int kWpt = kWords / kSelThreads;        // bitmap words per thread
     __shared__ unsigned bitmap[kWords];
-    __shared__ int wtot[kSelThreads / 32];
+    __shared__ int list_sh[33 * (kSelThreads / 32)];
+    extern __shared__ float rows_sm[];
+    const int scap = min(g.nbs, kSelCap);
     const int bg = blockIdx.x, b = bg / g.Hkv, kvh = bg % g.Hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = kSelThreads / 32;
     const int cap = g.nbs + 1;
@@ -258,7 +258,7 @@ decode_select_kernel(const int* __restrict__ kv_len, const float* __restrict__ x
         // no keys: the group's heads get a zero output and no work
         if (tid == 0) count[bg] = 0;
         for (int i = tid; i < g.G * g.d; i += kSelThreads) out[qrow0 * g.d + i] = __float2bfloat16(0.f);
-        if (nctas > 0) decode_plan_tail(count, offs, plan, hdr, g.B * g.Hkv, nctas);
+        if (nctas > 0) decode_plan_tail(count, offs, plan, hdr, g.B * g.Hkv, nctas, per);
         return;
     }
     const int bt = (L - 1) / kBlock;
@@ -268,27 +268,12 @@ decode_select_kernel(const int* __restrict__ kv_len, const float* __restrict__ x
     int no_conv = 0;
     for (int hl = warp; hl < g.G; hl += nwarp) {
         const size_t row = qrow0 + hl;
-        float t = __int_as_float(0x7fc00000);
         WarpRow xr;
-        xr.load(xs + row * cap, lane, bt);
-        if (bt > 0) {
-            float m = -INFINITY;
-            xr.each([&](int, float v) { m = fmaxf(m, v); });
-            m = warp_max(m);
-            HistBins* bins = hist_init ? &hist[warp] : nullptr;
-            t = alpha == 1.5f ? warp_row_tau<1>(xr, m, alpha, &no_conv, bins, g.maxit)
-              : alpha == 2.0f ? warp_row_tau<2>(xr, m, alpha, &no_conv, bins, g.maxit)
-                              : warp_row_tau<0>(xr, m, alpha, &no_conv, bins, g.maxit);
-        }
+        xr.load(xs + row * cap, rows_sm + (size_t)warp * scap, scap, lane, bt);
+        float t = __int_as_float(0x7fc00000);
+        if (bt > 0) t = row_tau(xr, xr.max(), alpha, &no_conv, hist_init ? &hist[warp] : nullptr, g.maxit);
         if (lane == 0) tau[row] = t;
-        float nsel = 0.f;
-        xr.each([&](int j, float v) {
-            if (v > t) {
-                nsel += 1.f;
-                atomicOr(&bitmap[j >> 5], 1u << (j & 31));
-            }
-        });
-        nsel = warp_sum(nsel);
+        const int nsel = xr.words(t, [&](int k, unsigned w) { atomicOr(&bitmap[k], w); });
         if (lane == 0) {
             atomicAdd(&hdr->selected_pairs, (unsigned long long)nsel);
             atomicAdd(&hdr->scored_pairs, (unsigned long long)bt);
@@ -296,47 +281,15 @@ decode_select_kernel(const int* __restrict__ kv_len, const float* __restrict__ x
     }
     if (no_conv) atomicOr(&hdr->status, kStNoConverge);
     __syncthreads();
-    // compaction: thread tid owns words tid * kWpt .. + kWpt - 1
-    unsigned wv[kWpt];
-    int pc = 0;
-#pragma unroll
-    for (int k = 0; k < kWpt; ++k) {
-        const int wi = tid * kWpt + k;
-        wv[k] = wi < nw ? bitmap[wi] : 0u;
-        pc += __popc(wv[k]);
-    }
-    int incl = pc;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += n;
-    }
-    if (lane == 31) wtot[warp] = incl;
-    __syncthreads();
-    int base = 0, total = 0;
-    for (int w = 0; w < nwarp; ++w) {
-        if (w < warp) base += wtot[w];
-        total += wtot[w];
-    }
-    int pos = base + incl - pc;
     int* dst = list + (size_t)bg * cap;
-#pragma unroll
-    for (int k = 0; k < kWpt; ++k) {
-        unsigned word = wv[k];
-        const int wi = tid * kWpt + k;
-        while (word) {
-            const int bit = __ffs(word) - 1;
-            dst[pos++] = wi * 32 + bit;
-            word &= word - 1;
-        }
-    }
+    const int total = bits_to_list([&](int i) { return bitmap[i]; }, nw, dst, list_sh, nwarp);
     if (tid == 0) {
         dst[total] = bt;                  // own block, always last
         count[bg] = total + 1;
         atomicAdd(&hdr->union_blocks, (unsigned long long)total);
         if (bt > 0) atomicAdd(&hdr->tiles, 1ull);
     }
-    if (nctas > 0) decode_plan_tail(count, offs, plan, hdr, g.B * g.Hkv, nctas);
+    if (nctas > 0) decode_plan_tail(count, offs, plan, hdr, g.B * g.Hkv, nctas, per);
 }
 
 template <int D>
@@ -507,7 +460,7 @@ decode_combine_kernel(const int* __restrict__ count, const float* __restrict__ p
 
 cudaError_t launch_decode_lists(const void* q, const float* ksum, const int* kv_len, void* out, const DecodeGeom& g,
                                 const DecodeGeom& gl, char* ws, float alpha, float coarse_scale, int nctas,
-                                cudaStream_t stream) {
+                                cudaStream_t stream, int per) {
     const float cx = (alpha - 1.0f) * coarse_scale / sqrtf((float)g.d);
     float* xs = reinterpret_cast<float*>(ws + gl.off_x);
     const auto* qb = static_cast<const __nv_bfloat16*>(q);
@@ -518,11 +471,14 @@ cudaError_t launch_decode_lists(const void* q, const float* ksum, const int* kv_
     // costs more than the passes it saves)
     const char* init = getenv("DASH_ENTMAX_INIT");
     const int hist_init = (init && strcmp(init, "histogram") == 0) ? 1 : 0;
-    decode_select_kernel<<<gl.B * gl.Hkv, kSelThreads, 0, stream>>>(
+    const int sm = (gl.nbs < kSelCap ? gl.nbs : kSelCap) * (kSelThreads / 32) * (int)sizeof(float);
+    const cudaError_t e = cudaFuncSetAttribute(decode_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+    if (e != cudaSuccess) return e;
+    decode_select_kernel<<<gl.B * gl.Hkv, kSelThreads, sm, stream>>>(
         kv_len, xs, reinterpret_cast<float*>(ws + gl.off_tau), reinterpret_cast<int*>(ws + gl.off_list),
         reinterpret_cast<int*>(ws + gl.off_count), reinterpret_cast<int*>(ws + gl.off_done),
         reinterpret_cast<int*>(ws + gl.off_offs), reinterpret_cast<int*>(ws + gl.off_plan),
-        static_cast<__nv_bfloat16*>(out), reinterpret_cast<WsHeader*>(ws), gl, alpha, nctas, hist_init);
+        static_cast<__nv_bfloat16*>(out), reinterpret_cast<WsHeader*>(ws), gl, alpha, nctas, per, hist_init);
     return cudaGetLastError();
 }
 

@@ -39,6 +39,8 @@ constexpr int kQ8Stages = 8;         // units in flight per CTA (two per consume
 constexpr int kQ8MaxG = 8;           // query heads per virtual group (one n8 tile)
 constexpr int kQ8Keys = 32;          // keys per unit
 constexpr int kQ8Tab = 64;           // list entries staged per table fill
+constexpr int kQ8Per = 4;            // list entries per CTA at least
+constexpr int kQ8PartHead = 4;       // floats of a partial before its output
 constexpr float kWBits = 12.0f;      // weights reach 2^12: f16 then keeps terms down to 2^-36 of the largest
 
 template <int D>
@@ -48,9 +50,9 @@ struct Q8Layout {
     static constexpr uint32_t kTx = kStage + 2 * kQ8Keys;       // with the scale bytes
     static constexpr uint32_t off_scale = kQ8Stages * kStage;   // [stage][K 32, V 32]
     static constexpr uint32_t off_merge = off_scale + kQ8Stages * 2 * kQ8Keys;
-    static constexpr uint32_t kRow = D + 3;                     // mA, sum, mB, output
-    static constexpr uint32_t merge_floats = kQ8Warps * kQ8MaxG * kRow > 2 * kDecodeMaxCtas * kQ8MaxG
-                                                 ? kQ8Warps * kQ8MaxG * kRow : 2 * kDecodeMaxCtas * kQ8MaxG;
+    static constexpr uint32_t kRow = kQ8PartHead + D;           // mA, sum, mB, -, output
+    static constexpr uint32_t merge_floats = kQ8Warps * kQ8MaxG * kRow > kDecodeMaxCtas * kQ8MaxG
+                                                 ? kQ8Warps * kQ8MaxG * kRow : kDecodeMaxCtas * kQ8MaxG;
     static constexpr uint32_t off_tab = off_merge + merge_floats * 4;
     static constexpr uint32_t tab_bytes = kQ8Tab * kQ8MaxG * 4 + kQ8Tab * 4;
     static constexpr uint32_t bytes = off_tab + tab_bytes + 1024;
@@ -95,7 +97,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     __shared__ float wa_sh[kQ8Warps][kQ8MaxG], inv_sh[kQ8MaxG];
     const int BH = g.B * g.Hkv, cap = g.nbs + 1;
     const long long U = offs[BH];
-    const int nC = (int)(U < (long long)gridDim.x ? U : (long long)gridDim.x), cta = blockIdx.x;
+    const int nC = split_ctas(U, (int)gridDim.x, kQ8Per), cta = blockIdx.x;
     if (cta >= nC) return;
     const int r_lo = (int)(U * cta / nC), r_hi = (int)(U * (cta + 1) / nC);
     const int bg_first = plan[cta];
@@ -193,13 +195,16 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // 2^-e_q in two factors (e_q may be as low as -147): q' is exact whatever q's size
             const int eq = amax > 0.f ? ilogbf(amax) - 14 : 0;
+            const int e1 = min(-eq, 127), e2 = -eq - e1;
+            const float s1 = __uint_as_float((unsigned)(e1 + 127) << 23), s2 = __uint_as_float((unsigned)(e2 + 127) << 23);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 float f[8];
                 bf16x8_to_float(w[c], f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = scalbnf(f[i], -eq);
+                for (int i = 0; i < 8; ++i) f[i] = f[i] * s1 * s2;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     qb[2 * c + i][0] = pack_f16(f[4 * i], f[4 * i + 1]);
@@ -387,8 +392,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             if (g4 == 0) { mrow[0] = ma[hh]; mrow[1] = l; mrow[2] = mb[hh]; }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                mrow[3 + g4 * NT * 2 + 2 * n] = o[n][hh];
-                mrow[3 + g4 * NT * 2 + 2 * n + 1] = o[n][2 + hh];
+                mrow[kQ8PartHead + g4 * NT * 2 + 2 * n] = o[n][hh];
+                mrow[kQ8PartHead + g4 * NT * 2 + 2 * n + 1] = o[n][2 + hh];
             }
         }
         cons_sync();
@@ -415,7 +420,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             inv_sh[tid] = den != 0.f ? exp2f(ub - ua - kWBits) / den : 0.f;
             if (!direct) {
                 float* pr = part + (slot * g.G + tid) * L::kRow;
-                pr[0] = MA; pr[1] = den; pr[2] = MB;
+                *reinterpret_cast<float4*>(pr) = make_float4(MA, den, MB, 0.f);
             }
         }
         cons_sync();
@@ -423,9 +428,9 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const int hl = idx / D, dim = idx % D;
             float acc = 0.f;
 #pragma unroll
-            for (int w = 0; w < kQ8Warps; ++w) acc = fmaf(merge[((size_t)w * kQ8MaxG + hl) * L::kRow + 3 + dim], wa_sh[w][hl], acc);
+            for (int w = 0; w < kQ8Warps; ++w) acc = fmaf(merge[((size_t)w * kQ8MaxG + hl) * L::kRow + kQ8PartHead + dim], wa_sh[w][hl], acc);
             if (direct) out[(qrow0 + hl) * D + dim] = __float2bfloat16(acc * inv_sh[hl]);
-            else part[(slot * g.G + hl) * L::kRow + 3 + dim] = acc;
+            else part[(slot * g.G + hl) * L::kRow + kQ8PartHead + dim] = acc;
         }
         if (!direct) {
             // the CTA that writes the group's last piece merges all of them
@@ -436,43 +441,56 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             cons_sync();
             if (ticket_sh == npieces - 1) {
                 __threadfence();
-                float* aw = merge;                               // [piece][head] mA, then its share of the sum
-                float* bw = aw + kDecodeMaxCtas * kQ8MaxG;       // [piece][head] mB, then weight
-                const size_t s0 = (size_t)c0 + bg;
-                const int np = npieces * g.G;
-                for (int i = tid; i < np; i += T) {
-                    const float* pp = part + (s0 * g.G + i) * L::kRow;
-                    aw[i] = __ldcg(pp);
-                    bw[i] = __ldcg(pp + 2);
-                }
-                cons_sync();
-                if (tid < g.G) {
-                    float MA = -INFINITY, MB = -INFINITY;
-                    for (int i = tid; i < np; i += g.G) {
-                        MA = fmaxf(MA, aw[i]);
-                        MB = fmaxf(MB, bw[i]);
+                // weights of the pieces, lanes over pieces; then the outputs, four dims per thread
+                // and many pieces' loads in flight (a piece at a time this merge took 20 us of the
+                // 16K step's 31)
+                const float* p0 = part + ((size_t)c0 + bg) * g.G * L::kRow;
+                const size_t pstep = (size_t)g.G * L::kRow;
+                for (int hl = warp; hl < g.G; hl += kQ8Warps) {
+                    float MA = -INFINITY, MB = -INFINITY, den = 0.f;
+                    for (int pc = lane; pc < npieces; pc += 32) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(p0 + pc * pstep + hl * L::kRow));
+                        MA = fmaxf(MA, v.x);
+                        MB = fmaxf(MB, v.z);
                     }
-                    wa_sh[0][tid] = MA == -INFINITY ? 0.f : MA;
-                    wa_sh[1][tid] = MB == -INFINITY ? 0.f : MB;
+                    MA = warp_max(MA);
+                    MB = warp_max(MB);
+                    const float ua = MA == -INFINITY ? 0.f : MA, ub = MB == -INFINITY ? 0.f : MB;
+                    for (int pc = lane; pc < npieces; pc += 32) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(p0 + pc * pstep + hl * L::kRow));
+                        den = fmaf(v.y, exp2f(v.x - ua), den);
+                        merge[pc * g.G + hl] = exp2f(v.z - ub);
+                    }
+                    den = warp_sum(den);
+                    if (lane == 0) inv_sh[hl] = den != 0.f ? exp2f(ub - ua - kWBits) / den : 0.f;
                 }
                 cons_sync();
-                for (int i = tid; i < np; i += T) {
-                    aw[i] = __ldcg(part + (s0 * g.G + i) * L::kRow + 1) * exp2f(aw[i] - wa_sh[0][i % g.G]);
-                    bw[i] = exp2f(bw[i] - wa_sh[1][i % g.G]);
+                constexpr int NO = kQ8MaxG * D / 4 / T;
+                float4 acc[NO];
+#pragma unroll
+                for (int k = 0; k < NO; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                for (int pc = 0; pc < npieces; ++pc) {
+#pragma unroll
+                    for (int k = 0; k < NO; ++k) {
+                        const int idx = tid + k * T, hl = idx / (D / 4), c = idx % (D / 4) * 4;
+                        if (hl < g.G) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(p0 + pc * pstep + hl * L::kRow + kQ8PartHead + c));
+                            const float wt = merge[pc * g.G + hl];
+                            acc[k].x = fmaf(v.x, wt, acc[k].x);
+                            acc[k].y = fmaf(v.y, wt, acc[k].y);
+                            acc[k].z = fmaf(v.z, wt, acc[k].z);
+                            acc[k].w = fmaf(v.w, wt, acc[k].w);
+                        }
+                    }
                 }
-                cons_sync();
-                if (tid < g.G) {
-                    float den = 0.f;
-                    for (int i = tid; i < np; i += g.G) den += aw[i];
-                    inv_sh[tid] = den != 0.f ? exp2f(wa_sh[1][tid] - wa_sh[0][tid] - kWBits) / den : 0.f;
-                }
-                cons_sync();
-                for (int idx = tid; idx < g.G * D; idx += T) {
-                    const int hl = idx / D, dim = idx % D;
-                    float acc = 0.f;
-                    for (int pc = 0; pc < npieces; ++pc)
-                        acc = fmaf(__ldcg(part + ((s0 + pc) * g.G + hl) * L::kRow + 3 + dim), bw[pc * g.G + hl], acc);
-                    out[(qrow0 + hl) * D + dim] = __float2bfloat16(acc * inv_sh[hl]);
+#pragma unroll
+                for (int k = 0; k < NO; ++k) {
+                    const int idx = tid + k * T, hl = idx / (D / 4), c = idx % (D / 4) * 4;
+                    if (hl < g.G) {
+                        const float f = inv_sh[hl];
+                        *reinterpret_cast<uint2*>(out + (qrow0 + hl) * D + c) = make_uint2(pack_bf16(acc[k].x * f, acc[k].y * f), pack_bf16(acc[k].z * f, acc[k].w * f));
+                    }
                 }
             }
         }
@@ -506,7 +524,7 @@ cudaError_t launch_decode_q8(const void* q, const void* kc, const void* vc, cons
                              const float* ksum, const int* kv_len, void* out, const DecodeQ8Geom& g, char* ws,
                              float alpha, float coarse_scale, cudaStream_t stream) {
     const int nctas = decode_tc_ctas();
-    cudaError_t e = launch_decode_lists(q, ksum, kv_len, out, g.real, g.v, ws, alpha, coarse_scale, nctas, stream);
+    cudaError_t e = launch_decode_lists(q, ksum, kv_len, out, g.real, g.v, ws, alpha, coarse_scale, nctas, stream, kQ8Per);
     if (e != cudaSuccess) return e;
     return g.v.d == 128 ? launch_attn<128>(q, kc, vc, ks, vs, kv_len, out, g, ws, alpha, nctas, stream)
                         : launch_attn<64>(q, kc, vc, ks, vs, kv_len, out, g, ws, alpha, nctas, stream);

@@ -7,30 +7,91 @@
 
 namespace dash {
 
-constexpr int kSelRegs = 48;        // row values a select lane keeps in registers
+constexpr int kSelCap = 1536;       // row values a warp keeps in shared memory at most
 
-// Row values of one head on one warp: lane l holds x[l + 32 k] for k < kSelRegs in
-// registers (-inf past the row's end, which no pass counts); values past that are read from
-// memory.
+// Row values of one row on one warp, in shared memory: lane l holds x[l + 32 k]; values past the
+// buffer are read from memory. 
 struct WarpRow {
-    float r[kSelRegs];
-    const float* p;
-    int lane, n;
-    __device__ __forceinline__ void load(const float* row, int ln, int count) {
-        p = row; lane = ln; n = count;
-#pragma unroll
-        for (int k = 0; k < kSelRegs; ++k) {
-            const int j = lane + 32 * k;
-            r[k] = j < n ? row[j] : -INFINITY;
-        }
+    const float *s, *p;
+    int lane, n, ns;
+    // buf: cap floats of this warp
+    __device__ __forceinline__ void load(const float* row, float* buf, int cap, int ln, int count) {
+        s = buf; p = row; lane = ln; n = count; ns = min(n, cap);
+        for (int j = lane; j < ns; j += 32) cp_async4(buf + j, row + j);
+        cp_async_commit();
+        cp_async_wait<0>();                            // a lane reads only what it copied
     }
     template <class F>
     __device__ __forceinline__ void each(F&& f) const {
-#pragma unroll
-        for (int k = 0; k < kSelRegs; ++k) f(lane + 32 * k, r[k]);
-        for (int j = lane + 32 * kSelRegs; j < n; j += 32) f(j, p[j]);
+        int j = lane;
+#pragma unroll 4
+        for (; j < ns; j += 32) f(j, s[j]);
+        for (; j < n; j += 32) f(j, p[j]);
+    }
+    __device__ __forceinline__ float max() const {
+        float m = -INFINITY;
+        each([&](int, float v) { m = fmaxf(m, v); });
+        return warp_max(m);
+    }
+    // Bitmap of the values above t: calls f(k, word) for every word k with a bit set, on the lane
+    // that holds it (a ballot over the lanes is a word; 32 words are gathered before their lanes
+    // act, so that no word waits for the one before).  Returns the number of bits; every lane
+    // calls it.
+    template <class F>
+    __device__ __forceinline__ int words(float t, F&& f) const {
+        int bits = 0;
+        for (int k0 = 0; k0 * 32 < n; k0 += 32) {
+            const int kn = min(32, (n - k0 * 32 + 31) / 32);
+            unsigned mine = 0u;
+#pragma unroll 4
+            for (int k = 0; k < kn; ++k) {
+                const int j = (k0 + k) * 32 + lane;
+                const unsigned w = __ballot_sync(0xffffffffu, j < n && (j < ns ? s[j] : p[j]) > t);
+                mine = lane == k ? w : mine;
+            }
+            bits += __popc(mine);
+            if (mine) f(k0 + lane, mine);
+        }
+        return warp_sum_int(bits);
     }
 };
+
+// Turns a bitmap of nw words into the ascending list of its bits at dst, by all warps of the CTA
+// (nwarp warps): a scan places the words, then a lane writes a bit.  word(i): word i; returns the
+// number of bits.  sh: 33 nwarp ints of shared memory.
+template <class W>
+__device__ __forceinline__ int bits_to_list(const W& word, int nw, int* dst, int* sh, int nwarp) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int* wtot = sh;
+    int* place = sh + nwarp;
+    int total = 0;
+    for (int w0 = 0; w0 < nw; w0 += nwarp * 32) {
+        const int wi = w0 + tid;
+        const int pc = wi < nw ? __popc(word(wi)) : 0;
+        int incl = pc;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) wtot[warp] = incl;
+        __syncthreads();
+        int pos = total + incl - pc;
+        for (int k = 0; k < nwarp; ++k) {
+            if (k < warp) pos += wtot[k];
+            total += wtot[k];
+        }
+        place[tid] = pos;
+        __syncthreads();
+        const int nb = min(nwarp * 32, nw - w0);
+        for (int k = warp; k < nb; k += nwarp) {
+            const unsigned w = word(w0 + k);
+            if ((w >> lane) & 1u) dst[place[k] + __popc(w & ((1u << lane) - 1u))] = (w0 + k) * 32 + lane;
+        }
+        __syncthreads();
+    }
+    return total;
+}
 
 constexpr int kHistBins = 64;       // bins of the histogram start over y = x - m in [-1, 0)
 
@@ -97,8 +158,7 @@ __device__ __forceinline__ float hist_start(const WarpRow& xr, float m, HistBins
 // bins != nullptr: start from the histogram edge (alpha = 1.5 and 2), else from u = -1.
 template <int MODE>
 __device__ __forceinline__ float warp_row_tau(const WarpRow& xr, float m, float alpha, int* no_conv,
-                                              HistBins* bins, int cap) {
-    float u0 = -1.0f;
+                                              HistBins* bins, int cap, float u0 = -1.0f) {
     if constexpr (MODE != 0) {
         if (bins) u0 = hist_start<MODE>(xr, m, bins);
     }
@@ -113,6 +173,39 @@ __device__ __forceinline__ float warp_row_tau(const WarpRow& xr, float m, float 
         if (sv.update(ps, &t, no_conv)) break;
     }
     return t;
+}
+
+// The threshold of a row whatever alpha is; m = its largest value, finite.
+__device__ __forceinline__ float row_tau(const WarpRow& xr, float m, float alpha, int* no_conv, HistBins* bins,
+                                         int cap, float u0 = -1.0f) {
+    return alpha == 1.5f ? warp_row_tau<1>(xr, m, alpha, no_conv, bins, cap, u0)
+         : alpha == 2.0f ? warp_row_tau<2>(xr, m, alpha, no_conv, bins, cap, u0)
+                         : warp_row_tau<0>(xr, m, alpha, no_conv, bins, cap, u0);
+}
+
+// A start below the root from the lanes' 32 largest values (a subset's root never exceeds the
+// row's, entmax.cuh): one value per lane, so its passes cost a reduction each, and a few passes
+// over the row are left of the eight or so from u = -1.
+template <int MODE>
+__device__ __forceinline__ float lane_start_t(float y, float alpha) {
+    EntmaxSolver sv;
+    sv.init(0.0f, alpha);
+    float t = -1.0f;
+    int nc = 0;
+    for (int it = 0; it < 24; ++it) {
+        EntmaxPass ps;
+        ps.reset();
+        ps.add_t<MODE>(y - sv.u, sv.e);
+        ps.warp_reduce_t<MODE>();
+        if (sv.update(ps, &t, &nc)) return (nc || !(t >= -1.0f)) ? sv.lo : fminf(t, -1e-30f);
+    }
+    return sv.lo;
+}
+__device__ __forceinline__ float lane_start(const WarpRow& xr, float m, float alpha) {
+    float y = -INFINITY;
+    xr.each([&](int, float v) { y = fmaxf(y, v); });
+    y -= m;
+    return alpha == 1.5f ? lane_start_t<1>(y, alpha) : alpha == 2.0f ? lane_start_t<2>(y, alpha) : lane_start_t<0>(y, alpha);
 }
 
 // Work plan of the balanced attention pass, built by the last select CTA to finish (a

@@ -35,6 +35,8 @@ namespace dash {
 // a free permutation of the dims, so each lane loads 8 consecutive dims of its row at once:
 // slots (2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9) of steps 2 c and 2 c + 1 are dims
 // 32 c + 8 t4 + 0 .. 7.
+constexpr int kScoreRows = 64;       // query rows per CTA
+
 template <int D>
 __device__ __forceinline__ void tree_score_chunk(const __nv_bfloat16* q, const float* ksum, float* xs, const TreeGeom& g,
                                                  int bg, int F, int j0, float cx) {
@@ -62,109 +64,125 @@ __device__ __forceinline__ void tree_score_chunk(const __nv_bfloat16* q, const f
         }
     }
     const size_t row0 = (size_t)bg * g.R;                           // rows of a KV group are contiguous in q
-    for (int r0 = 0; r0 < g.R; r0 += 8) {
-        const int rq = min(r0 + g4, g.R - 1);
-        const uint4* qr = reinterpret_cast<const uint4*>(q + (row0 + rq) * D) + t4;
+    const int r_lo = (int)blockIdx.z * kScoreRows, r_hi = min(g.R, r_lo + kScoreRows);
+    auto load_q = [&](uint4 (&v)[D / 32], int r0) {
+        const uint4* qr = reinterpret_cast<const uint4*>(q + (row0 + min(r0 + g4, g.R - 1)) * D) + t4;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) v[c] = __ldg(qr + c * 4);
+    };
+    uint4 v[D / 32], nv[D / 32];
+    load_q(v, r_lo);
+    for (int r0 = r_lo; r0 < r_hi; r0 += 8) {
+        load_q(nv, r0 + 8);                                         // the next rows on their way
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-            const uint4 v = __ldg(qr + c * 4);
-            mma_bf16(acc, hi[2 * c], v.x, v.y);
-            mma_bf16(acc, lo[2 * c], v.x, v.y);
-            mma_bf16(acc, hi[2 * c + 1], v.z, v.w);
-            mma_bf16(acc, lo[2 * c + 1], v.z, v.w);
+            mma_bf16(acc, hi[2 * c], v[c].x, v[c].y);
+            mma_bf16(acc, lo[2 * c], v[c].x, v[c].y);
+            mma_bf16(acc, hi[2 * c + 1], v[c].z, v[c].w);
+            mma_bf16(acc, lo[2 * c + 1], v[c].z, v[c].w);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = r0 + 2 * t4 + (i & 1), j = jw + g4 + 8 * (i >> 1);
-            if (r < g.R && j < F) xs[(row0 + r) * g.cap + j] = acc[i] * cx;
+            if (r < r_hi && j < F) xs[(row0 + r) * g.cap + j] = acc[i] * cx;
         }
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) v[c] = nv[c];
     }
 }
 
+// Row y = 0 of the grid prepares a KV group: ancestor sets, depths, the tiles' empty bitmaps and,
+// where some path completes the open block, the sum of the open block's keys on every path.
 template <int D, bool Q8>
 __global__ void __launch_bounds__(128)
-tree_scores_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ kd,
-                   const int* __restrict__ parent, const int* __restrict__ n_nodes, const void* __restrict__ kc,
-                   const uint8_t* __restrict__ ks, const float* __restrict__ ksum, const int* __restrict__ kv_len,
-                   float* __restrict__ xs, unsigned long long* __restrict__ anc, int* __restrict__ depth,
-                   unsigned* __restrict__ bits, int* __restrict__ tick, TreeGeom g, float cx) {
+tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
     __shared__ int par_s[kMaxNodes], dep_s[kMaxNodes];
-    __shared__ float path[kMaxNodes][D];
-    const int bg = blockIdx.x, b = bg / g.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ float path[kMaxNodes][D], tail_s[D];
+    const int bg = blockIdx.x, b = bg / g.Hkv, tid = threadIdx.x;
     int L, nodes;
-    const bool live = tree_live(kv_len, n_nodes, g, b, &L, &nodes);
+    const bool live = tree_live(a.kv_len, a.n_nodes, g, b, &L, &nodes);
     const int F = live ? L / kBlock : 0;
     if (blockIdx.y > 0) {
         const int j0 = ((int)blockIdx.y - 1) * 64;
-        if (j0 < F) tree_score_chunk<D>(q, ksum, xs, g, bg, F, j0, cx);
+        if (j0 < F) tree_score_chunk<D>(static_cast<const __nv_bfloat16*>(a.q), a.ksum, w.xs, g, bg, F, j0, cx);
         return;
     }
+    if (blockIdx.z > 0) return;
     // the group's tiles start with nothing selected
-    for (int i = tid; i < g.tiles_bg * g.nbw; i += 128) bits[(size_t)bg * g.tiles_bg * g.nbw + i] = 0u;
-    for (int i = tid; i < g.tiles_bg; i += 128) tick[bg * g.tiles_bg + i] = 0;
-    // ancestor sets and depths: every node walks up its path (parents come before children, so
-    // the walk ends); a parent outside [-1, i) makes the node and its descendants invalid
-    for (int i = tid; i < nodes; i += 128) par_s[i] = parent[(size_t)b * g.N + i];
+    for (int i = tid; i < g.tiles_bg * g.nbw; i += 128) w.bits[(size_t)bg * g.tiles_bg * g.nbw + i] = 0u;
+    for (int i = tid; i < g.tiles_bg; i += 128) w.tick[bg * g.tiles_bg + i] = 0;
+    // every node walks up its path (parents come before children, so the walk ends); a parent
+    // outside [-1, i) makes the node and its descendants invalid
+    for (int i = tid; i < nodes; i += 128) par_s[i] = a.parent[(size_t)b * g.N + i];
     __syncthreads();
     if (tid < g.N) {
-        unsigned long long a = 0ull;
+        unsigned long long m = 0ull;
         int dp = -1;
         if (live && tid < nodes) {
             int i = tid;
             while (i >= 0) {
                 const int p = par_s[i];
-                if (p < -1 || p >= i) { a = 0ull; dp = -1; break; }
-                a |= 1ull << i;
+                if (p < -1 || p >= i) { m = 0ull; dp = -1; break; }
+                m |= 1ull << i;
                 ++dp;
                 i = p;
             }
         }
         dep_s[tid] = dp;
-        if (bg % g.Hkv == 0) { anc[(size_t)b * g.N + tid] = a; depth[(size_t)b * g.N + tid] = dp; }
+        if (bg % g.Hkv == 0) { w.anc[(size_t)b * g.N + tid] = m; w.depth[(size_t)b * g.N + tid] = dp; }
     }
-    __syncthreads();
-    if (!live) return;
     const int r = L % kBlock;
-    int any = 0;
-    for (int i = tid; i < nodes; i += 128) any |= r + dep_s[i] >= kBlock;
-    any = __syncthreads_or(any);
-    const size_t row0 = (size_t)bg * g.R;
-    if (any) {
-        // path[i] = the sum of the open block's keys on node i's path (all its tokens with
-        // r + depth < 64), every dim a recurrence over the nodes
-        for (int c = tid; c < D; c += 128) {
-            float tail = 0.f;
-            for (int t = L - r; t < L; ++t) {
-                const size_t o = ((size_t)bg * g.Tmax + t);
-                if constexpr (Q8) {
-                    float f[4];
-                    e4m3x4_to_float(static_cast<const uint8_t*>(kc)[o * D + c], scale_value(ks[o]), f);
-                    tail += f[0];
-                } else {
-                    tail += __bfloat162float(static_cast<const __nv_bfloat16*>(kc)[o * D + c]);
-                }
-            }
-            for (int i = 0; i < nodes; ++i) {
-                const int p = par_s[i];
-                if (dep_s[i] < 0) continue;
-                float v = p >= 0 ? path[p][c] : tail;
-                if (r + dep_s[i] < kBlock) v += __bfloat162float(kd[((size_t)bg * g.N + i) * D + c]);
-                path[i][c] = v;
-            }
-        }
-        __syncthreads();
+    if (!__syncthreads_or(live && tid < g.N && r + dep_s[tid < g.N ? tid : 0] >= kBlock)) return;
+    // path[i] = the cached keys of the open block, and the path's tokens in it (r + depth < 64): all
+    // rows loaded at once, then one addition per node down the tree, a thread per dim
+    if (tid < D) tail_s[tid] = 0.f;
+    __syncthreads();
+    const auto* kd = static_cast<const __nv_bfloat16*>(a.k_draft) + (size_t)bg * g.N * D;
+    for (int i = tid; i < nodes * (D / 8); i += 128) {
+        float f[8];
+        bf16x8_to_float(__ldg(reinterpret_cast<const uint4*>(kd) + i), f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) path[i / (D / 8)][i % (D / 8) * 8 + c] = f[c];
     }
-    for (int row = warp; row < g.R; row += 4) {
-        const int node = row % g.N;
-        const bool crossed = node < nodes && dep_s[node] >= 0 && r + dep_s[node] >= kBlock;
-        float x = -INFINITY;
-        if (crossed) {
-            float s = 0.f;
-            for (int c = lane; c < D; c += 32) s = fmaf(__bfloat162float(q[(row0 + row) * D + c]), path[node][c], s);
-            x = warp_sum(s) * (cx / kBlock);
+    {
+        // 4 dims per thread; D / 4 threads cover a row, the rows of the open block go round robin
+        constexpr int TPR = D / 4, NR = 128 / TPR;
+        const int c = tid % TPR * 4, r0 = tid / TPR;
+        const size_t row0 = (size_t)bg * g.Tmax + (L - r);
+        float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int i = r0; i < r; i += NR) {
+            float f[4];
+            if constexpr (Q8) {
+                e4m3x4_to_float(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.k_cache) + (row0 + i) * D + c),
+                                scale_value(static_cast<const uint8_t*>(a.k_scale)[row0 + i]), f);
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.k_cache) + (row0 + i) * D + c);
+                const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+                const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+                f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[k] += f[k];
         }
-        if (lane == 0) xs[(row0 + row) * g.cap + F] = x;
+        // row groups add in a fixed order
+        for (int gq = 0; gq < NR; ++gq) {
+            if (r0 == gq)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tail_s[c + k] += t[k];
+            __syncthreads();
+        }
+    }
+    float* dst = w.path + (size_t)bg * g.N * D;
+    if (tid < D) {
+        for (int i = 0; i < nodes; ++i) {
+            if (dep_s[i] < 0) continue;
+            const float up = par_s[i] >= 0 ? path[par_s[i]][tid] : tail_s[tid];
+            const float v = r + dep_s[i] < kBlock ? up + path[i][tid] : up;
+            path[i][tid] = v;
+            dst[(size_t)i * D + tid] = v;
+        }
     }
 }
 
@@ -177,12 +195,10 @@ tree_scores_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __r
 constexpr int kTreeSelWarps = 8;
 
 __global__ void __launch_bounds__(kTreeSelWarps * 32)
-tree_select_kernel(const int* __restrict__ kv_len, const int* __restrict__ n_nodes, const float* __restrict__ xs,
-                   const unsigned long long* __restrict__ anc, const int* __restrict__ depth, float* __restrict__ tau,
-                   unsigned* __restrict__ bits, int* __restrict__ tick, int* __restrict__ list, int* __restrict__ count,
-                   int* __restrict__ offs, int* __restrict__ plan, __nv_bfloat16* __restrict__ out,
-                   WsHeader* __restrict__ hdr, TreeGeom g, float alpha, int nctas, int per) {
-    __shared__ int last_sh, wtot[kTreeSelWarps];
+tree_select_kernel(TreeArgs a, TreeWork w, TreeGeom g, float alpha, float cx, int nctas, int per) {
+    __shared__ int last_sh, list_sh[33 * kTreeSelWarps];
+    extern __shared__ float rows_sm[];
+    const int scap = min(g.cap, kSelCap);
     constexpr int kCtasPerTile = kTreeRows / kTreeSelWarps;
     const int tile = blockIdx.x / kCtasPerTile, sub = blockIdx.x % kCtasPerTile;
     const int bg = tile / g.tiles_bg, b = bg / g.Hkv;
@@ -190,94 +206,71 @@ tree_select_kernel(const int* __restrict__ kv_len, const int* __restrict__ n_nod
     if (sub * kTreeSelWarps >= rows) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int L, nodes;
-    const bool live = tree_live(kv_len, n_nodes, g, b, &L, &nodes);
+    const bool live = tree_live(a.kv_len, a.n_nodes, g, b, &L, &nodes);
     const int F = live ? L / kBlock : 0, r = live ? L % kBlock : 0;
     const int lrow = sub * kTreeSelWarps + warp;                     // row of the tile
     if (lrow < rows) {
         const size_t row = (size_t)bg * g.R + r0 + lrow;
         const int node = (r0 + lrow) % g.N;
-        const int dp = depth[(size_t)b * g.N + node];
-        if (node < (n_nodes ? min(n_nodes[b], g.N) : g.N) && (!live || dp < 0)) {
+        const int dp = w.depth[(size_t)b * g.N + node];
+        if (node < (a.n_nodes ? min(a.n_nodes[b], g.N) : g.N) && (!live || dp < 0)) {
             // no valid length or parent: zero output
-            for (int c = lane; c < g.d; c += 32) out[row * g.d + c] = __float2bfloat16(0.f);
+            for (int c = lane; c < g.d; c += 32) static_cast<__nv_bfloat16*>(a.out)[row * g.d + c] = __float2bfloat16(0.f);
         }
         float t = __int_as_float(0x7fc00000);
         if (live && dp >= 0) {
-            const int n = F + (r + dp >= kBlock ? 1 : 0);
+            const bool crossed = r + dp >= kBlock;
+            const int n = F + (crossed ? 1 : 0);
+            float* xrow = w.xs + row * g.cap;
+            if (crossed) {
+                // the path completes the open block: its score from the mean of the block's 64 keys
+                const auto* qr = static_cast<const __nv_bfloat16*>(a.q) + row * g.d;
+                const float* pr = w.path + ((size_t)bg * g.N + node) * g.d;
+                float s = 0.f;
+                for (int c = lane; c < g.d; c += 32) s = fmaf(__bfloat162float(qr[c]), pr[c], s);
+                s = warp_sum(s) * (cx / kBlock);
+                if (lane == (F & 31)) xrow[F] = s;               // the lane that reads it below
+            }
+            int no_conv = 0, nsel = 0;
             WarpRow xr;
-            xr.load(xs + row * g.cap, lane, n);
-            float m = -INFINITY;
-            xr.each([&](int, float v) { m = fmaxf(m, v); });
-            m = warp_max(m);
-            int no_conv = 0;
-            if (m > -INFINITY)
-                t = alpha == 1.5f ? warp_row_tau<1>(xr, m, alpha, &no_conv, nullptr, g.maxit)
-                  : alpha == 2.0f ? warp_row_tau<2>(xr, m, alpha, &no_conv, nullptr, g.maxit)
-                                  : warp_row_tau<0>(xr, m, alpha, &no_conv, nullptr, g.maxit);
-            if (no_conv && lane == 0) atomicOr(&hdr->status, kStNoConverge);
-            int nsel = 0;
-            const int words = (n + 31) / 32;
-            auto word = [&](int k, float v) {
-                const unsigned w = __ballot_sync(0xffffffffu, v > t);
-                nsel += __popc(w);
-                if (w && lane == 0) atomicOr(&bits[(size_t)tile * g.nbw + k], w);
-            };
-#pragma unroll
-            for (int k = 0; k < kSelRegs; ++k)
-                if (k < words) word(k, xr.r[k]);
-            for (int k = kSelRegs; k < words; ++k) word(k, lane + 32 * k < n ? xr.p[lane + 32 * k] : -INFINITY);
+            xr.load(xrow, rows_sm + (size_t)warp * scap, scap, lane, n);
+            const float m = xr.max();
+            if (m > -INFINITY) t = row_tau(xr, m, alpha, &no_conv, nullptr, g.maxit, lane_start(xr, m, alpha));
+            nsel = xr.words(t, [&](int k, unsigned sel) { atomicOr(&w.bits[(size_t)tile * g.nbw + k], sel); });
             if (lane == 0) {
-                atomicAdd(&hdr->selected_pairs, (unsigned long long)nsel);
-                atomicAdd(&hdr->scored_pairs, (unsigned long long)n);
+                if (no_conv) atomicOr(&w.hdr->status, kStNoConverge);
+                atomicAdd(&w.hdr->selected_pairs, (unsigned long long)nsel);
+                atomicAdd(&w.hdr->scored_pairs, (unsigned long long)n);
             }
         }
-        if (lane == 0) tau[row] = t;
+        if (lane == 0) w.tau[row] = t;
     }
     __syncthreads();
     if (tid == 0) {
         __threadfence();
-        last_sh = atomicAdd(&tick[tile], 1) == (rows + kTreeSelWarps - 1) / kTreeSelWarps - 1;
+        last_sh = atomicAdd(&w.tick[tile], 1) == (rows + kTreeSelWarps - 1) / kTreeSelWarps - 1;
     }
     __syncthreads();
     if (!last_sh) return;
     __threadfence();
-    int* dst = list + (size_t)tile * g.lcap;
+    int* dst = w.list + (size_t)tile * g.lcap;
     int total = 0;
     if (live) {
-        const int nw = (F + 31) / 32;
-        for (int w0 = 0; w0 < nw; w0 += kTreeSelWarps * 32) {
-            const int wi = w0 + tid;
-            unsigned word = wi < nw ? __ldcg(bits + (size_t)tile * g.nbw + wi) : 0u;
-            if (wi == F / 32) word &= (1u << (F & 31)) - 1u;         // the open block has its own entry
-            const int pc = __popc(word);
-            int incl = pc;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            if (lane == 31) wtot[warp] = incl;
-            __syncthreads();
-            int pos = total + incl - pc;
-            for (int w = 0; w < kTreeSelWarps; ++w) {
-                if (w < warp) pos += wtot[w];
-                total += wtot[w];
-            }
-            while (word) {
-                dst[pos++] = wi * 32 + __ffs(word) - 1;
-                word &= word - 1;
-            }
-            __syncthreads();
-        }
+        // the open block has its own entry
+        auto word = [&](int i) {
+            const unsigned m = __ldcg(w.bits + (size_t)tile * g.nbw + i);
+            return i == F / 32 ? m & ((1u << (F & 31)) - 1u) : m;
+        };
+        total = bits_to_list(word, (F + 31) / 32, dst, list_sh, kTreeSelWarps);
         if (tid == 0) {
-            atomicAdd(&hdr->union_blocks, (unsigned long long)total);
-            if (total > 0) atomicAdd(&hdr->tiles, 1ull);
+            atomicAdd(&w.hdr->union_blocks, (unsigned long long)total);
+            if (total > 0) atomicAdd(&w.hdr->tiles, 1ull);
             if (r > 0) dst[total++] = kTreeOpen;
             dst[total++] = kTreeDraft;
         }
     }
-    if (tid == 0) count[tile] = total;
-    decode_plan_tail(count, offs, plan, hdr, g.tiles, nctas, per);
+    if (tid == 0) w.count[tile] = total;
+    decode_plan_tail(w.count, w.offs, w.plan, w.hdr, g.tiles, nctas, per);
 }
 
 // ------------------------------------------------------------------ host side
@@ -297,18 +290,15 @@ static cudaError_t launch_tree_t(const TreeArgs& a, const TreeGeom& g, char* ws,
     const float cx = (alpha - 1.0f) * coarse_scale / sqrtf((float)D);
     const float e_pow = 1.0f / (alpha - 1.0f), sm2 = 1.4426950408889634f / sqrtf((float)D);
     const TreeWork w = tree_work(g, ws);
-    const auto* q = static_cast<const __nv_bfloat16*>(a.q);
-    const auto* kd = static_cast<const __nv_bfloat16*>(a.k_draft);
-    const auto* ks = static_cast<const uint8_t*>(a.k_scale);
-    auto* out = static_cast<__nv_bfloat16*>(a.out);
-    const dim3 gs((unsigned)(g.B * g.Hkv), (unsigned)((g.nbs + 63) / 64 + 1));
+    const dim3 gs((unsigned)(g.B * g.Hkv), (unsigned)((g.nbs + 63) / 64 + 1), (unsigned)((g.R + kScoreRows - 1) / kScoreRows));
     const int nctas = tree_ctas();
-    tree_scores_kernel<D, Q8><<<gs, 128, 0, stream>>>(q, kd, a.parent, a.n_nodes, a.k_cache, ks, a.ksum, a.kv_len, w.xs, w.anc,
-                                                      w.depth, w.bits, w.tick, g, cx);
-    tree_select_kernel<<<(unsigned)g.tiles * (kTreeRows / kTreeSelWarps), kTreeSelWarps * 32, 0, stream>>>(
-        a.kv_len, a.n_nodes, w.xs, w.anc, w.depth, w.tau, w.bits, w.tick, w.list, w.count, w.offs, w.plan, out, w.hdr, g, alpha,
-        nctas, kTreePer);
-    const cudaError_t e = cudaGetLastError();
+    tree_scores_kernel<D, Q8><<<gs, 128, 0, stream>>>(a, w, g, cx);
+    const int sm = (g.cap < kSelCap ? g.cap : kSelCap) * kTreeSelWarps * (int)sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(tree_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+    if (e != cudaSuccess) return e;
+    tree_select_kernel<<<(unsigned)g.tiles * (kTreeRows / kTreeSelWarps), kTreeSelWarps * 32, sm, stream>>>(a, w, g, alpha, cx, nctas,
+                                                                                                      kTreePer);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_tree_attn(a, w, g, e_pow, sm2, nctas, kTreePer, stream);
 }

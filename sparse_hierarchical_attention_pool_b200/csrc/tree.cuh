@@ -14,9 +14,10 @@ struct TreeWork {
     float *xs, *tau;                     // scores [rows][cap], thresholds
     unsigned long long* anc;             // [B][N] ancestors and self (0: an invalid node)
     int* depth;                          // [B][N]
+    float* path;                         // [B Hkv][N][D] sum of the open block's keys on a node's path
     unsigned* bits;                      // [tile][nbw] selected blocks
     int *tick, *list, *count, *offs, *plan;
-    float* part;                         // [CTA + tile][128][D + 2]
+    float* part;                         // [CTA + tile][128][max, sum, -, -, output D]
 };
 
 inline TreeWork tree_work(const TreeGeom& g, char* ws) {
@@ -26,6 +27,7 @@ inline TreeWork tree_work(const TreeGeom& g, char* ws) {
     w.tau = reinterpret_cast<float*>(ws + g.off_tau);
     w.anc = reinterpret_cast<unsigned long long*>(ws + g.off_anc);
     w.depth = reinterpret_cast<int*>(ws + g.off_depth);
+    w.path = reinterpret_cast<float*>(ws + g.off_path);
     w.bits = reinterpret_cast<unsigned*>(ws + g.off_bits);
     w.tick = reinterpret_cast<int*>(ws + g.off_tick);
     w.list = reinterpret_cast<int*>(ws + g.off_list);

@@ -19,7 +19,7 @@
 // draft's behind its nodes) are overwritten with zeros before the product: weight 0 times
 // whatever they hold would not be 0 if that were NaN.
 // 8-bit cache: warp 8 streams codes and scale bytes with bulk copies into a ring of their own,
-// and warps 12 - 15 turn them into the bf16 operand tiles (exact: cache8.cuh) or load the
+// and warps 12, 13 (K) and 14, 15 (V) turn them into the bf16 operand tiles (exact: cache8.cuh) or load the
 // draft's bf16 rows.
 // Every wait is bounded; a CTA that gives up sets a status bit.
 #include "cache8.cuh"
@@ -99,7 +99,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const auto* q = static_cast<const __nv_bfloat16*>(a.q);
     if (tid == 0) {
         abort_sh = 0;
-        const int conv = Q8 ? 128 : 1;                          // who fills an operand tile
+        const int conv = Q8 ? 64 : 1;                           // who fills an operand tile
         mbar_init(bar(B_Q), 256);
         for (int i = 0; i < KS; ++i) { mbar_init(bar(B_KF + i), conv); mbar_init(bar(B_KE + i), 1); }
         for (int i = 0; i < VS; ++i) { mbar_init(bar(B_VF + i), conv); mbar_init(bar(B_VE + i), 1); }
@@ -310,8 +310,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     } else if (warp >= 12) {
         // ------------------------------------------------------------ converters (8-bit cache)
         if constexpr (Q8) {
-            constexpr int CH = D / 16;                           // 16-code chunks per row
-            const int ct = tid - 384;
+            // two warps for K and two for V, each pair at its own ring's pace: V tiles are free
+            // only after their product, K tiles long before
+            constexpr int CH = D / 16, NS = kTtK;                // 16-code chunks per row
+            const int kv = (warp - 12) >> 1, ct = tid & 63;
+            const int bF = kv ? (int)B_VF : (int)B_KF, bE = kv ? (int)B_VE : (int)B_KE;
+            const auto* draft_rows = static_cast<const __nv_bfloat16*>(kv ? a.v_draft : a.k_draft);
             bool ok = true;
             int rs = 0;                                          // raw stages taken
             segments([&](int tile, int e0, int n, int gs0) {
@@ -319,55 +323,47 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 int len, nodes;
                 tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes);
                 for (int s = 0; s < n; ++s) {
-                    const int gs = gs0 + s;
+                    const int gs = gs0 + s, st = gs % NS, rst = rs % kTtRaw;
                     const int j = w.list[(size_t)tile * g.lcap + e0 + s];
                     const bool draft = j == kTreeDraft;
                     const int lim = draft ? nodes : j == kTreeOpen ? len % kBlock : kBlock;   // rows that are there
-                    const int rst = rs % kTtRaw;
                     if (!draft) {
                         ok = ok && mbar_wait(bar(B_RF + rst), (rs / kTtRaw) & 1, abort_flag);
                         ++rs;
                     }
+                    ok = ok && (gs < NS || mbar_wait(bar(bE + st), ((gs / NS) - 1) & 1, abort_flag));
+                    if (!ok) continue;
                     const uint8_t* rp = base_ptr + L::off_raw + rst * L::kRaw;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        constexpr int NS = kTtK;
-                        const int st = gs % NS;
-                        ok = ok && (gs < NS || mbar_wait(bar((kv ? (int)B_VE : (int)B_KE) + st), ((gs / NS) - 1) & 1, abort_flag));
-                        if (ok) {
-                            uint8_t* dst = base_ptr + (kv ? L::off_v : L::off_k) + st * L::kTile;
-                            const auto* dr = static_cast<const __nv_bfloat16*>(kv ? a.v_draft : a.k_draft) + (size_t)bg * g.N * D;
-#pragma unroll
-                            for (int it = 0; it < kBlock * CH / 128; ++it) {
-                                const int idx = it * 128 + ct, r = idx / CH, c = idx % CH;
-                                uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-                                if (r < lim) {
-                                    if (draft) {
-                                        const uint4* p = reinterpret_cast<const uint4*>(dr + (size_t)r * D) + c * 2;
-                                        lo = __ldg(p);
-                                        hi = __ldg(p + 1);
-                                    } else {
-                                        const uint4 x = *reinterpret_cast<const uint4*>(rp + kv * L::kRawKV + idx * 16);
-                                        const float fs = scale_value(rp[2 * L::kRawKV + kv * 64 + r]);
-                                        const __nv_bfloat162 f = __floats2bfloat162_rn(fs, fs);
-                                        e4m3x4_to_bf16x4(x.x, f, &lo.x, &lo.y);
-                                        e4m3x4_to_bf16x4(x.y, f, &lo.z, &lo.w);
-                                        e4m3x4_to_bf16x4(x.z, f, &hi.x, &hi.y);
-                                        e4m3x4_to_bf16x4(x.w, f, &hi.z, &hi.w);
-                                    }
-                                }
-                                // chunks 2 c and 2 c + 1 of the row's half; the upper half's lanes store the
-                                // odd chunk first, so the lanes of a phase fall in distinct banks
-                                uint8_t* row = dst + (c >> 2) * L::kHalf + r * 128;
-                                const int c0 = (c & 3) * 2, sw = c >> 2;
-                                *reinterpret_cast<uint4*>(row + (((c0 + sw) ^ (r & 7)) << 4)) = sw ? hi : lo;
-                                *reinterpret_cast<uint4*>(row + (((c0 + 1 - sw) ^ (r & 7)) << 4)) = sw ? lo : hi;
+                    uint8_t* dst = base_ptr + (kv ? L::off_v : L::off_k) + st * L::kTile;
+#pragma unroll 4
+                    for (int it = 0; it < kBlock * CH / 64; ++it) {
+                        const int idx = it * 64 + ct, r = idx / CH, c = idx % CH;
+                        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+                        if (r < lim) {
+                            if (draft) {
+                                const uint4* p = reinterpret_cast<const uint4*>(draft_rows + ((size_t)bg * g.N + r) * D) + c * 2;
+                                lo = __ldg(p);
+                                hi = __ldg(p + 1);
+                            } else {
+                                const uint4 x = *reinterpret_cast<const uint4*>(rp + kv * L::kRawKV + idx * 16);
+                                const float fs = scale_value(rp[2 * L::kRawKV + kv * 64 + r]);
+                                const __nv_bfloat162 f = __floats2bfloat162_rn(fs, fs);
+                                e4m3x4_to_bf16x4(x.x, f, &lo.x, &lo.y);
+                                e4m3x4_to_bf16x4(x.y, f, &lo.z, &lo.w);
+                                e4m3x4_to_bf16x4(x.z, f, &hi.x, &hi.y);
+                                e4m3x4_to_bf16x4(x.w, f, &hi.z, &hi.w);
                             }
-                            fence_proxy_async_smem();
-                            mbar_arrive(bar((kv ? (int)B_VF : (int)B_KF) + st));
                         }
+                        // chunks 2 c and 2 c + 1 of the row's half; the upper half's lanes store the
+                        // odd chunk first, so the lanes of a phase fall in distinct banks
+                        uint8_t* row = dst + (c >> 2) * L::kHalf + r * 128;
+                        const int c0 = (c & 3) * 2, sw = c >> 2;
+                        *reinterpret_cast<uint4*>(row + (((c0 + sw) ^ (r & 7)) << 4)) = sw ? hi : lo;
+                        *reinterpret_cast<uint4*>(row + (((c0 + 1 - sw) ^ (r & 7)) << 4)) = sw ? lo : hi;
                     }
-                    if (!draft && ok) mbar_arrive(bar(B_RE + rst));
+                    fence_proxy_async_smem();
+                    mbar_arrive(bar(bF + st));
+                    if (!draft) mbar_arrive(bar(B_RE + rst));
                 }
             });
         }
@@ -547,7 +543,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 const float den = (w0 > 0.f ? l0 * w0 : 0.f) + (w1 > 0.f ? l1 * w1 : 0.f);
                 const int o0 = w.offs[tile], o1 = w.offs[tile + 1];
                 const bool direct = dt_cta_of(o0, U, nC) == dt_cta_of(o1 - 1, U, nC);
-                float* pr = w.part + (((size_t)cta + tile) * kTreeRows + r) * (D + 2);
+                float* pr = w.part + (((size_t)cta + tile) * kTreeRows + r) * (D + 4);
                 if (!direct && valid && grp == 0) { pr[0] = M; pr[1] = den; }
                 const float inv = direct ? 1.0f / den : 1.0f;
                 auto* out = static_cast<__nv_bfloat16*>(a.out) + row * D;
@@ -579,7 +575,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                             }
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) *reinterpret_cast<float2*>(pr + 2 + col + 2 * i) = make_float2(f[2 * i], f[2 * i + 1]);
+                            for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(pr + 4 + col + 4 * i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
                         }
                     }
                 }
@@ -616,30 +612,37 @@ tree_combine_kernel(TreeArgs a, TreeWork w, TreeGeom g, int nctas, int per) {
     if (!tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes)) return;
     const int node = row_g % g.N;
     if (node >= nodes || !w.anc[(size_t)b * g.N + node]) return;
-    const float* p = w.part + (((size_t)c0 + tile) * kTreeRows + r) * (D + 2);
-    const size_t step = (size_t)kTreeRows * (D + 2);
+    const float* p = w.part + (((size_t)c0 + tile) * kTreeRows + r) * (D + 4);
+    const size_t step = (size_t)kTreeRows * (D + 4);
     const int np = c1 - c0 + 1;
-    float M = -INFINITY;
+    float M = -INFINITY, den = 0.f;
     for (int i = lane; i < np; i += 32) M = fmaxf(M, __ldcg(p + i * step));
     M = warp_max(M);
-    float num[DPL], den = 0.f;
+    float num[DPL];
 #pragma unroll
     for (int d = 0; d < DPL; ++d) num[d] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < np; ++i) {
-        const float* pi = p + i * step;
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(pi));
-        float v[DPL];
-#pragma unroll
-        for (int d = 0; d < DPL / 2; ++d) {
-            const float2 t = __ldcg(reinterpret_cast<const float2*>(pi + 2 + lane * DPL + 2 * d));
-            v[2 * d] = t.x; v[2 * d + 1] = t.y;
+    for (int i0 = 0; i0 < np; i0 += 32) {
+        // lane i holds piece i's weight
+        float wt = 0.f;
+        if (i0 + lane < np) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + (i0 + lane) * step));
+            wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+            den = fmaf(ml.y, wt, den);
         }
-        const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-        den = fmaf(ml.y, wt, den);
+        const int kn = min(32, np - i0);
+#pragma unroll 8
+        for (int k = 0; k < kn; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, wt, k);
+            const float* pi = p + (i0 + k) * step + 4 + lane * DPL;
 #pragma unroll
-        for (int d = 0; d < DPL; ++d) num[d] = fmaf(v[d], wt, num[d]);
+            for (int d = 0; d < DPL / 2; ++d) {
+                const float2 t = __ldcg(reinterpret_cast<const float2*>(pi) + d);
+                num[2 * d] = fmaf(t.x, wk, num[2 * d]);
+                num[2 * d + 1] = fmaf(t.y, wk, num[2 * d + 1]);
+            }
+        }
     }
+    den = warp_sum(den);
     const float inv = 1.0f / den;
     auto* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)bg * g.R + row_g) * D + lane * DPL;
 #pragma unroll

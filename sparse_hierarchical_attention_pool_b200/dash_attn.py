@@ -499,60 +499,54 @@ _U8 = torch.uint8
 _E4M3 = torch.float8_e4m3fn
 
 
-class _On:
-    """The current device set to the tensors' one for a call (they must all share it)."""
-
-    def __init__(self, *tensors):
-        devs = {t.device for t in tensors if isinstance(t, torch.Tensor)}
-        if len(devs) != 1:
-            raise ValueError(f"tensors on more than one device: {sorted(map(str, devs))}")
-        dev = devs.pop()
-        if dev.type != "cuda":
-            raise ValueError("tensors must be CUDA tensors")
-        self.guard = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
-
-    def __enter__(self):
-        if self.guard:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard:
-            self.guard.__exit__(*exc)
-
-
-def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
+def _refuse(t, dtype, shape, dev, name):
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on device {t.get_device()}, the call's first tensor on {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _lens(t, B, name):
-    """An optional int32 [B] device argument."""
-    if t is None:
-        return None
-    _shape(t, (B,), name)
-    return _dev(t, torch.int32, name)
+def _ptr(t, dtype, shape, dev, name):
+    """Address of a contiguous tensor of this type and shape on device index `dev`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        _refuse(t, dtype, shape, dev, name)
+    return t.data_ptr()
 
 
-def _cache8(k_cache, v_cache, k_scale, v_scale):
-    B, Hkv, Tmax, d = k_cache.shape
-    _shape(v_cache, (B, Hkv, Tmax, d), "v_cache")
-    _shape(k_scale, (B, Hkv, Tmax), "k_scale")
-    _shape(v_scale, (B, Hkv, Tmax), "v_scale")
-    return (_dev(k_cache, _E4M3, "k_cache"), _dev(v_cache, _E4M3, "v_cache"), _dev(k_scale, _U8, "k_scale"),
-            _dev(v_scale, _U8, "v_scale"))
+def _opt(t, dtype, shape, dev, name):
+    return None if t is None else _ptr(t, dtype, shape, dev, name)
 
 
-def _ksum(ksum, B, Hkv, Tmax, d, block):
+def _ksum(ksum, B, Hkv, Tmax, d, block, dev):
     """Block summaries [B, Hkv, Tmax // block, d] (one row at least, as dash_block_summary makes them)."""
-    if tuple(ksum.shape) not in {(B, Hkv, Tmax // block, d), (B, Hkv, max(Tmax // block, 1), d)}:
-        raise ValueError(f"ksum must be [B, Hkv, Tmax // {block}, d], got {list(ksum.shape)}")
-    return _dev(ksum, torch.float32, "ksum")
+    n = Tmax // block
+    return _ptr(ksum, torch.float32, (B, Hkv, n if n or ksum.shape[2] == 0 else 1, d), dev, "ksum")
 
 
-def _space(workspace, need, device):
+def _run(name, dev, stream, *args):
+    """Call a library function with the tensors' device current, on `stream` or that device's
+    current stream."""
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    fn = getattr(lib(), name)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc != DASH_OK:
+        raise DashError(name, rc)
+
+
+def _space(workspace, size, dims, device):
+    """The caller's workspace, or a new one of size(*dims) bytes."""
     if workspace is None:
-        return alloc_workspace(need, device)
-    if workspace.device != device or workspace.dtype != _U8 or not workspace.is_contiguous():
+        return alloc_workspace(size(*dims), device)
+    if workspace.device != device or workspace.dtype is not _U8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
     return workspace
 
@@ -577,20 +571,16 @@ def dash_cache_append(k_new, v_new, kv_len, k_cache, v_cache, k_scale, v_scale, 
     ksum fp32 [B, Hkv, Tmax // 64, d] or None: the blocks this completes get their means."""
     B, Hkv, rows, d = k_new.shape
     Tmax = k_cache.shape[2]
-    _shape(v_new, k_new.shape, "v_new")
-    _shape(k_cache, (B, Hkv, Tmax, d), "k_cache")
-    if src is not None:
-        n = src.shape[1] if n is None else n
-        _shape(src, (B, n), "src")
-    n = rows if n is None else n
-    with _On(k_new, v_new, kv_len, k_cache, v_cache, k_scale, v_scale, ksum, n_new, src):
-        kc, vc, ks, vs = _cache8(k_cache, v_cache, k_scale, v_scale)
-        _check("dash_cache_append", lib().dash_cache_append(
-            _dev(k_new, torch.bfloat16, "k_new"), _dev(v_new, torch.bfloat16, "v_new"),
-            None if src is None else _dev(src, torch.int32, "src"), _lens(n_new, B, "n_new"),
-            _lens(kv_len, B, "kv_len"), kc, vc, ks, vs,
-            None if ksum is None else _ksum(ksum, B, Hkv, Tmax, d, block), B, Hkv, rows, n, Tmax, d, block,
-            _stream(stream)))
+    if n is None:
+        n = rows if src is None else src.shape[1]
+    dev, full, flat = k_new.get_device(), (B, Hkv, Tmax, d), (B, Hkv, Tmax)
+    _run("dash_cache_append", dev, stream,
+         _ptr(k_new, torch.bfloat16, k_new.shape, dev, "k_new"), _ptr(v_new, torch.bfloat16, k_new.shape, dev, "v_new"),
+         _opt(src, torch.int32, (B, n), dev, "src"), _opt(n_new, torch.int32, (B,), dev, "n_new"),
+         _ptr(kv_len, torch.int32, (B,), dev, "kv_len"),
+         _ptr(k_cache, _E4M3, full, dev, "k_cache"), _ptr(v_cache, _E4M3, full, dev, "v_cache"),
+         _ptr(k_scale, _U8, flat, dev, "k_scale"), _ptr(v_scale, _U8, flat, dev, "v_scale"),
+         None if ksum is None else _ksum(ksum, B, Hkv, Tmax, d, block, dev), B, Hkv, rows, n, Tmax, d, block)
 
 
 def dash_cache_read(k_cache, v_cache, k_scale, v_scale, n, start=None, kv_len=None, k_out=None, v_out=None,
@@ -598,17 +588,17 @@ def dash_cache_read(k_cache, v_cache, k_scale, v_scale, n, start=None, kv_len=No
     """Rows start[b] .. start[b] + n - 1 of the 8-bit cache as bf16 (k, v) [B, Hkv, n, d]; rows at or
     behind kv_len[b] are zero.  start, kv_len int32 [B] (None: 0 and Tmax)."""
     B, Hkv, Tmax, d = k_cache.shape
-    k_out = torch.empty(B, Hkv, n, d, dtype=torch.bfloat16, device=k_cache.device) if k_out is None else k_out
-    v_out = torch.empty(B, Hkv, n, d, dtype=torch.bfloat16, device=k_cache.device) if v_out is None else v_out
-    _shape(k_out, (B, Hkv, n, d), "k_out")
-    _shape(v_out, (B, Hkv, n, d), "v_out")
-    if n == 0:
-        return k_out, v_out
-    with _On(k_cache, v_cache, k_scale, v_scale, start, kv_len, k_out, v_out):
-        _check("dash_cache_read", lib().dash_cache_read(
-            *_cache8(k_cache, v_cache, k_scale, v_scale), _lens(start, B, "start"), _lens(kv_len, B, "kv_len"),
-            _dev(k_out, torch.bfloat16, "k_out"), _dev(v_out, torch.bfloat16, "v_out"), B, Hkv, n, Tmax, d, block,
-            _stream(stream)))
+    dev, full, flat, rows = k_cache.get_device(), (B, Hkv, Tmax, d), (B, Hkv, Tmax), (B, Hkv, n, d)
+    if k_out is None:
+        k_out = torch.empty(rows, dtype=torch.bfloat16, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty(rows, dtype=torch.bfloat16, device=k_cache.device)
+    args = (_ptr(k_cache, _E4M3, full, dev, "k_cache"), _ptr(v_cache, _E4M3, full, dev, "v_cache"),
+            _ptr(k_scale, _U8, flat, dev, "k_scale"), _ptr(v_scale, _U8, flat, dev, "v_scale"),
+            _opt(start, torch.int32, (B,), dev, "start"), _opt(kv_len, torch.int32, (B,), dev, "kv_len"),
+            _ptr(k_out, torch.bfloat16, rows, dev, "k_out"), _ptr(v_out, torch.bfloat16, rows, dev, "v_out"))
+    if n > 0:
+        _run("dash_cache_read", dev, stream, *args, B, Hkv, n, Tmax, d, block)
     return k_out, v_out
 
 
@@ -631,17 +621,17 @@ def dash_decode_q8(q, k_cache, v_cache, k_scale, v_scale, ksum, kv_len, out=None
     """One decode step over the 8-bit cache: q bf16 [B, Hq, d].  Returns (out, workspace)."""
     B, Hq, d = q.shape
     Hkv, Tmax = k_cache.shape[1], k_cache.shape[2]
-    _shape(k_cache, (B, Hkv, Tmax, d), "k_cache")
-    out = torch.empty_like(q) if out is None else out
-    _shape(out, q.shape, "out")
-    with _On(q, k_cache, v_cache, k_scale, v_scale, ksum, kv_len, out):
-        if workspace is None or workspace.device != q.device or workspace.dtype != _U8:
-            workspace = _space(workspace, decode_q8_workspace_size(B, Hq, Hkv, Tmax, d, block), q.device)
-        _check("dash_decode_q8", lib().dash_decode_q8(
-            _dev(q, torch.bfloat16, "q"), *_cache8(k_cache, v_cache, k_scale, v_scale),
-            _ksum(ksum, B, Hkv, Tmax, d, block), _lens(kv_len, B, "kv_len"), _dev(out, torch.bfloat16, "out"),
-            B, Hq, Hkv, Tmax, d, block, float(alpha), float(coarse_scale),
-            ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _stream(stream)))
+    dev, full, flat = q.get_device(), (B, Hkv, Tmax, d), (B, Hkv, Tmax)
+    if out is None:
+        out = torch.empty_like(q)
+    args = (_ptr(q, torch.bfloat16, q.shape, dev, "q"),
+            _ptr(k_cache, _E4M3, full, dev, "k_cache"), _ptr(v_cache, _E4M3, full, dev, "v_cache"),
+            _ptr(k_scale, _U8, flat, dev, "k_scale"), _ptr(v_scale, _U8, flat, dev, "v_scale"),
+            _ksum(ksum, B, Hkv, Tmax, d, block, dev), _ptr(kv_len, torch.int32, (B,), dev, "kv_len"),
+            _ptr(out, torch.bfloat16, q.shape, dev, "out"))
+    workspace = _space(workspace, decode_q8_workspace_size, (B, Hq, Hkv, Tmax, d, block), q.device)
+    _run("dash_decode_q8", dev, stream, *args, B, Hq, Hkv, Tmax, d, block, alpha, coarse_scale,
+         workspace.data_ptr(), workspace.numel())
     return out, workspace
 
 
@@ -649,24 +639,20 @@ def _tree(name, q, k_draft, v_draft, parent, k_cache, v_cache, scales, ksum, kv_
           coarse_scale, workspace, block, stream):
     B, Hq, N, d = q.shape
     Hkv, Tmax = k_cache.shape[1], k_cache.shape[2]
-    _shape(k_cache, (B, Hkv, Tmax, d), "k_cache")
-    _shape(v_cache, (B, Hkv, Tmax, d), "v_cache")
-    _shape(k_draft, (B, Hkv, N, d), "k_draft")
-    _shape(v_draft, (B, Hkv, N, d), "v_draft")
-    _shape(parent, (B, N), "parent")
-    out = torch.empty_like(q) if out is None else out
-    _shape(out, q.shape, "out")
-    with _On(q, k_draft, v_draft, parent, k_cache, v_cache, *scales, ksum, kv_len, n_nodes, out):
-        if workspace is None or workspace.device != q.device or workspace.dtype != _U8:
-            workspace = _space(workspace, decode_tree_workspace_size(B, Hq, Hkv, N, Tmax, d, block), q.device)
-        cache = _cache8(k_cache, v_cache, *scales) if scales else (
-            _dev(k_cache, torch.bfloat16, "k_cache"), _dev(v_cache, torch.bfloat16, "v_cache"))
-        _check(name, getattr(lib(), name)(
-            _dev(q, torch.bfloat16, "q"), _dev(k_draft, torch.bfloat16, "k_draft"),
-            _dev(v_draft, torch.bfloat16, "v_draft"), _dev(parent, torch.int32, "parent"),
-            _lens(n_nodes, B, "n_nodes"), *cache, _ksum(ksum, B, Hkv, Tmax, d, block), _lens(kv_len, B, "kv_len"),
-            _dev(out, torch.bfloat16, "out"), B, Hq, Hkv, N, Tmax, d, block, float(alpha), float(coarse_scale),
-            ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _stream(stream)))
+    dev, full, flat, draft = q.get_device(), (B, Hkv, Tmax, d), (B, Hkv, Tmax), (B, Hkv, N, d)
+    if out is None:
+        out = torch.empty_like(q)
+    kind = _E4M3 if scales else torch.bfloat16
+    args = (_ptr(q, torch.bfloat16, q.shape, dev, "q"),
+            _ptr(k_draft, torch.bfloat16, draft, dev, "k_draft"), _ptr(v_draft, torch.bfloat16, draft, dev, "v_draft"),
+            _ptr(parent, torch.int32, (B, N), dev, "parent"), _opt(n_nodes, torch.int32, (B,), dev, "n_nodes"),
+            _ptr(k_cache, kind, full, dev, "k_cache"), _ptr(v_cache, kind, full, dev, "v_cache"),
+            *[_ptr(t, _U8, flat, dev, "k_scale / v_scale") for t in scales],
+            _ksum(ksum, B, Hkv, Tmax, d, block, dev), _ptr(kv_len, torch.int32, (B,), dev, "kv_len"),
+            _ptr(out, torch.bfloat16, q.shape, dev, "out"))
+    workspace = _space(workspace, decode_tree_workspace_size, (B, Hq, Hkv, N, Tmax, d, block), q.device)
+    _run(name, dev, stream, *args, B, Hq, Hkv, N, Tmax, d, block, alpha, coarse_scale,
+         workspace.data_ptr(), workspace.numel())
     return out, workspace
 
 
