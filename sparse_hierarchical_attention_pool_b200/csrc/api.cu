@@ -496,10 +496,8 @@ int dash_decode_q8(const void* q, const void* k_cache, const void* v_cache, cons
     DecodeQ8Geom g;
     if (block != kBlock || !make_decode_q8_geom(B, Hq, Hkv, Tmax, d, &g)) return DASH_ERR_SHAPE;
     if (!workspace || !al256(workspace) || ws_bytes < g.v.total) return DASH_ERR_WORKSPACE;
-    char* ws = static_cast<char*>(workspace);
-    if (cudaMemsetAsync(ws, 0, sizeof(WsHeader), S(stream)) != cudaSuccess) return DASH_ERR_CUDA;
-    return launch_decode_q8(q, k_cache, v_cache, k_scale, v_scale, ksum, kv_len, out, g, ws, alpha, coarse_scale,
-                            S(stream)) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+    return launch_decode_q8(q, k_cache, v_cache, k_scale, v_scale, ksum, kv_len, out, g, static_cast<char*>(workspace),
+                            alpha, coarse_scale, S(stream)) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ drafted-token trees
@@ -522,9 +520,7 @@ static int tree_impl(const TreeArgs& a, bool q8, int B, int Hq, int Hkv, int N, 
     TreeGeom g;
     if (block != kBlock || !make_tree_geom(B, Hq, Hkv, N, Tmax, d, &g) || (q8 && Tmax % kBlock)) return DASH_ERR_SHAPE;
     if (!workspace || !al256(workspace) || ws_bytes < g.total) return DASH_ERR_WORKSPACE;
-    char* ws = static_cast<char*>(workspace);
-    if (cudaMemsetAsync(ws, 0, sizeof(WsHeader), S(stream)) != cudaSuccess) return DASH_ERR_CUDA;
-    return launch_tree(a, g, ws, alpha, coarse_scale, S(stream)) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+    return launch_tree(a, g, static_cast<char*>(workspace), alpha, coarse_scale, S(stream)) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
 int dash_decode_tree(const void* q, const void* k_draft, const void* v_draft, const int* parent, const int* n_nodes,

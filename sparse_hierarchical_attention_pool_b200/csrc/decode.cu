@@ -70,11 +70,19 @@ struct ScoreShape {
     static constexpr int LOGV = V >= 32 ? 5 : V >= 16 ? 4 : V >= 8 ? 3 : V >= 4 ? 2 : V >= 2 ? 1 : 0;
 };
 
+// The first block of a step's first kernel clears the workspace header (hdr null: the caller did).
+__device__ __forceinline__ void clear_header(WsHeader* hdr, bool first) {
+    if (hdr && first && threadIdx.x < sizeof(WsHeader) / 16) reinterpret_cast<uint4*>(hdr)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 template <int D, int GP>
 __global__ void __launch_bounds__(256)
 decode_scores_kernel(const __nv_bfloat16* __restrict__ q, const float* __restrict__ ksum,
-                     const int* __restrict__ kv_len, float* __restrict__ xs, DecodeGeom g, float cx) {
+                     const int* __restrict__ kv_len, float* __restrict__ xs, DecodeGeom g, float cx,
+                     WsHeader* __restrict__ hdr) {
     using S = ScoreShape<D, GP>;
+    clear_header(hdr, blockIdx.x == 0);
+    pdl_trigger();
     const int lane = threadIdx.x & 31;
     const long long wtask = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int tpg = (g.nbs + S::RW - 1) / S::RW;
@@ -154,7 +162,10 @@ decode_scores_kernel(const __nv_bfloat16* __restrict__ q, const float* __restric
 template <int D>
 __global__ void __launch_bounds__(256)
 decode_scores_wide_kernel(const __nv_bfloat16* __restrict__ q, const float* __restrict__ ksum,
-                          const int* __restrict__ kv_len, float* __restrict__ xs, DecodeGeom g, float cx) {
+                          const int* __restrict__ kv_len, float* __restrict__ xs, DecodeGeom g, float cx,
+                          WsHeader* __restrict__ hdr) {
+    clear_header(hdr, blockIdx.x == 0 && blockIdx.y == 0);
+    pdl_trigger();
     constexpr int QD = D / 4;                 // dims per thread
     constexpr int QV = QD / 4;                // float4 per thread
     constexpr int QS = D + 16;                // padded row stride of a query head (floats)
@@ -208,23 +219,23 @@ decode_scores_wide_kernel(const __nv_bfloat16* __restrict__ q, const float* __re
 
 template <int D, int GP>
 void launch_scores_gp(const __nv_bfloat16* q, const float* ksum, const int* kv_len, float* xs,
-                      const DecodeGeom& g, float cx, cudaStream_t stream) {
+                      const DecodeGeom& g, float cx, WsHeader* hdr, cudaStream_t stream) {
     using S = ScoreShape<D, GP>;
     const long long warps = (long long)g.B * g.Hkv * ((g.nbs + S::RW - 1) / S::RW);
     const unsigned grid = (unsigned)((warps + 7) / 8);
-    if (grid > 0) decode_scores_kernel<D, GP><<<grid, 256, 0, stream>>>(q, ksum, kv_len, xs, g, cx);
+    if (grid > 0) decode_scores_kernel<D, GP><<<grid, 256, 0, stream>>>(q, ksum, kv_len, xs, g, cx, hdr);
 }
 
 template <int D>
 void launch_scores(const __nv_bfloat16* q, const float* ksum, const int* kv_len, float* xs,
-                   const DecodeGeom& g, float cx, cudaStream_t stream) {
-    if (g.G == 1) launch_scores_gp<D, 1>(q, ksum, kv_len, xs, g, cx, stream);
-    else if (g.G == 2) launch_scores_gp<D, 2>(q, ksum, kv_len, xs, g, cx, stream);
-    else if (g.G <= 4) launch_scores_gp<D, 4>(q, ksum, kv_len, xs, g, cx, stream);
-    else if (g.G <= 8) launch_scores_gp<D, 8>(q, ksum, kv_len, xs, g, cx, stream);
+                   const DecodeGeom& g, float cx, WsHeader* hdr, cudaStream_t stream) {
+    if (g.G == 1) launch_scores_gp<D, 1>(q, ksum, kv_len, xs, g, cx, hdr, stream);
+    else if (g.G == 2) launch_scores_gp<D, 2>(q, ksum, kv_len, xs, g, cx, hdr, stream);
+    else if (g.G <= 4) launch_scores_gp<D, 4>(q, ksum, kv_len, xs, g, cx, hdr, stream);
+    else if (g.G <= 8) launch_scores_gp<D, 8>(q, ksum, kv_len, xs, g, cx, hdr, stream);
     else {
         dim3 gs(g.B * g.Hkv, (g.nbs + 63) / 64 > 0 ? (g.nbs + 63) / 64 : 1);
-        decode_scores_wide_kernel<D><<<gs, 256, 0, stream>>>(q, ksum, kv_len, xs, g, cx);
+        decode_scores_wide_kernel<D><<<gs, 256, 0, stream>>>(q, ksum, kv_len, xs, g, cx, hdr);
     }
 }
 
@@ -241,7 +252,7 @@ decode_select_kernel(const int* __restrict__ kv_len, const float* __restrict__ x
                      float* __restrict__ tau, int* __restrict__ list, int* __restrict__ count,
                      int* __restrict__ done, int* __restrict__ offs, int* __restrict__ plan,
                      __nv_bfloat16* __restrict__ out, WsHeader* __restrict__ hdr, DecodeGeom g,
-                     float alpha, int nctas, int per, int hist_init) {
+                     float alpha, int nctas, int hist_init) {
     constexpr int kWords = kMaxT / kBlock / 32;
     __shared__ HistBins hist[kSelThreads / 32];
     __shared__ unsigned bitmap[kWords];
@@ -253,12 +264,14 @@ decode_select_kernel(const int* __restrict__ kv_len, const float* __restrict__ x
     const int cap = g.nbs + 1;
     const int L = kv_len[b];
     const size_t qrow0 = (size_t)b * g.Hq + (size_t)kvh * g.G;
+    pdl_trigger();
+    pdl_wait();
     if (tid == 0) done[bg] = 0;
     if (L < 1 || L > g.Tmax) {
         // no keys: the group's heads get a zero output and no work
         if (tid == 0) count[bg] = 0;
         for (int i = tid; i < g.G * g.d; i += kSelThreads) out[qrow0 * g.d + i] = __float2bfloat16(0.f);
-        if (nctas > 0) decode_plan_tail(count, offs, plan, hdr, g.B * g.Hkv, nctas, per);
+        if (nctas > 0) decode_plan_tail(count, offs, plan, hdr, g.B * g.Hkv, nctas);
         return;
     }
     const int bt = (L - 1) / kBlock;
@@ -289,7 +302,7 @@ decode_select_kernel(const int* __restrict__ kv_len, const float* __restrict__ x
         atomicAdd(&hdr->union_blocks, (unsigned long long)total);
         if (bt > 0) atomicAdd(&hdr->tiles, 1ull);
     }
-    if (nctas > 0) decode_plan_tail(count, offs, plan, hdr, g.B * g.Hkv, nctas, per);
+    if (nctas > 0) decode_plan_tail(count, offs, plan, hdr, g.B * g.Hkv, nctas);
 }
 
 template <int D>
@@ -460,26 +473,29 @@ decode_combine_kernel(const int* __restrict__ count, const float* __restrict__ p
 
 cudaError_t launch_decode_lists(const void* q, const float* ksum, const int* kv_len, void* out, const DecodeGeom& g,
                                 const DecodeGeom& gl, char* ws, float alpha, float coarse_scale, int nctas,
-                                cudaStream_t stream, int per) {
+                                cudaStream_t stream, bool pdl) {
     const float cx = (alpha - 1.0f) * coarse_scale / sqrtf((float)g.d);
     float* xs = reinterpret_cast<float*>(ws + gl.off_x);
     const auto* qb = static_cast<const __nv_bfloat16*>(q);
-    if (g.d == 128) launch_scores<128>(qb, ksum, kv_len, xs, g, cx, stream);
-    else launch_scores<64>(qb, ksum, kv_len, xs, g, cx, stream);
+    WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
+    if (g.d == 128) launch_scores<128>(qb, ksum, kv_len, xs, g, cx, pdl ? hdr : nullptr, stream);
+    else launch_scores<64>(qb, ksum, kv_len, xs, g, cx, pdl ? hdr : nullptr, stream);
     // DASH_ENTMAX_INIT=histogram starts each threshold solve at the histogram edge; the
     // default, Newton from u = -1, is faster on the rows measured here (the binning pass
     // costs more than the passes it saves)
     const char* init = getenv("DASH_ENTMAX_INIT");
     const int hist_init = (init && strcmp(init, "histogram") == 0) ? 1 : 0;
     const int sm = (gl.nbs < kSelCap ? gl.nbs : kSelCap) * (kSelThreads / 32) * (int)sizeof(float);
-    const cudaError_t e = cudaFuncSetAttribute(decode_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+    cudaError_t e = cudaFuncSetAttribute(decode_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
     if (e != cudaSuccess) return e;
-    decode_select_kernel<<<gl.B * gl.Hkv, kSelThreads, sm, stream>>>(
-        kv_len, xs, reinterpret_cast<float*>(ws + gl.off_tau), reinterpret_cast<int*>(ws + gl.off_list),
-        reinterpret_cast<int*>(ws + gl.off_count), reinterpret_cast<int*>(ws + gl.off_done),
-        reinterpret_cast<int*>(ws + gl.off_offs), reinterpret_cast<int*>(ws + gl.off_plan),
-        static_cast<__nv_bfloat16*>(out), reinterpret_cast<WsHeader*>(ws), gl, alpha, nctas, per, hist_init);
-    return cudaGetLastError();
+    PdlConfig c(gl.B * gl.Hkv, kSelThreads, sm, stream);
+    if (!pdl) c.cfg.numAttrs = 0;
+    e = cudaLaunchKernelEx(&c.cfg, decode_select_kernel, kv_len, (const float*)xs, reinterpret_cast<float*>(ws + gl.off_tau),
+                           reinterpret_cast<int*>(ws + gl.off_list), reinterpret_cast<int*>(ws + gl.off_count),
+                           reinterpret_cast<int*>(ws + gl.off_done), reinterpret_cast<int*>(ws + gl.off_offs),
+                           reinterpret_cast<int*>(ws + gl.off_plan), static_cast<__nv_bfloat16*>(out), hdr, gl, alpha, nctas,
+                           hist_init);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_decode(const void* q, const void* kc, const void* vc, const float* ksum,

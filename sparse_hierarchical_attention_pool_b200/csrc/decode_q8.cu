@@ -84,7 +84,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 2)
 decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vs,
                  const int* __restrict__ kv_len, const float* __restrict__ xs, const float* __restrict__ tau,
-                 const int* __restrict__ list, const int* __restrict__ offs, const int* __restrict__ plan,
+                 const int* __restrict__ list, const int* __restrict__ count,
                  float* __restrict__ part, int* __restrict__ done, __nv_bfloat16* __restrict__ out,
                  WsHeader* __restrict__ hdr, DecodeGeom g, int split, float e_pow, float sm2) {
     using L = Q8Layout<D>;
@@ -95,13 +95,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     __shared__ __align__(8) uint64_t full[kQ8Stages], empty[kQ8Stages];
     __shared__ int abort_sh, ticket_sh;
     __shared__ float wa_sh[kQ8Warps][kQ8MaxG], inv_sh[kQ8MaxG];
-    const int BH = g.B * g.Hkv, cap = g.nbs + 1;
-    const long long U = offs[BH];
-    const int nC = split_ctas(U, (int)gridDim.x, kQ8Per), cta = blockIdx.x;
-    if (cta >= nC) return;
-    const int r_lo = (int)(U * cta / nC), r_hi = (int)(U * (cta + 1) / nC);
-    const int bg_first = plan[cta];
-
+    __shared__ int share_sh[kQ8Warps + 3];
+    const int cap = g.nbs + 1, cta = blockIdx.x;
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* const base_ptr = smem_raw + (base - raw);
@@ -113,19 +108,24 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             mbar_init(smem_u32(&empty[s]), 1);
         }
         fence_mbar_init();
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
     }
-    __syncthreads();
+    pdl_wait();
+    // the barriers are visible after list_share's barriers
+    const ListShare sh = list_share<(kQ8Warps + 1) * 32>(count, g.B * g.Hkv, cta, (int)gridDim.x, kQ8Per, share_sh);
+    if (sh.lo >= sh.hi) return;                        // whole CTA: nothing listed for it
+    const long long U = sh.U;
+    const int nC = sh.nC, r_hi = sh.hi;
     volatile int* abort_flag = &abort_sh;
 
     if (warp == kQ8Warps) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
-            prefetch_tmap(&tm_k);
-            prefetch_tmap(&tm_v);
             long long cnt = 0;
             bool ok = true;
-            for (int bg = bg_first, pos = r_lo; ok && pos < r_hi; ++bg) {
-                const int o0 = offs[bg], o1 = offs[bg + 1];
+            for (int bg = sh.first, pos = sh.lo, o0 = sh.o_first, o1; ok && pos < r_hi; ++bg, o0 = o1) {
+                o1 = o0 + __ldcg(count + bg);
                 if (o1 <= pos) continue;
                 const int seg_hi = min(r_hi, o1);
                 for (int e = pos - o0; e < seg_hi - o0 && ok; ++e) {
@@ -169,8 +169,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     auto cons_sync = [&]() { asm volatile("bar.sync 1, %0;" :: "n"(T) : "memory"); };
     long long cnt = 0;
     bool ok = true;
-    for (int bg = bg_first, pos = r_lo; pos < r_hi; ++bg) {
-        const int o0 = offs[bg], o1 = offs[bg + 1];
+    for (int bg = sh.first, pos = sh.lo, o0 = sh.o_first, o1; pos < r_hi; ++bg, o0 = o1) {
+        o1 = o0 + __ldcg(count + bg);
         if (o1 <= pos) continue;
         const int seg_hi = min(r_hi, o1);
         const int e_lo = pos - o0, e_hi = seg_hi - o0;
@@ -510,21 +510,22 @@ static cudaError_t launch_attn(const void* q, const void* kc, const void* vc, co
     const int sm = (int)Q8Layout<D>::bytes;
     cudaError_t e = cudaFuncSetAttribute(decode_q8_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
     if (e != cudaSuccess) return e;
-    decode_q8_kernel<D><<<nctas, (kQ8Warps + 1) * 32, sm, stream>>>(
-        tk, tv, static_cast<const __nv_bfloat16*>(q), static_cast<const uint8_t*>(ks), static_cast<const uint8_t*>(vs), kv_len,
-        reinterpret_cast<const float*>(ws + g.off_x), reinterpret_cast<const float*>(ws + g.off_tau),
-        reinterpret_cast<const int*>(ws + g.off_list), reinterpret_cast<const int*>(ws + g.off_offs),
-        reinterpret_cast<const int*>(ws + g.off_plan), reinterpret_cast<float*>(ws + g.off_part),
-        reinterpret_cast<int*>(ws + g.off_done), static_cast<__nv_bfloat16*>(out), reinterpret_cast<WsHeader*>(ws), g,
-        gq.split, 1.0f / (alpha - 1.0f), 1.4426950408889634f / sqrtf((float)D));
-    return cudaGetLastError();
+    const PdlConfig c(nctas, (kQ8Warps + 1) * 32, sm, stream);
+    e = cudaLaunchKernelEx(&c.cfg, decode_q8_kernel<D>, tk, tv, static_cast<const __nv_bfloat16*>(q),
+                           static_cast<const uint8_t*>(ks), static_cast<const uint8_t*>(vs), kv_len,
+                           reinterpret_cast<const float*>(ws + g.off_x), reinterpret_cast<const float*>(ws + g.off_tau),
+                           reinterpret_cast<const int*>(ws + g.off_list), reinterpret_cast<const int*>(ws + g.off_count),
+                           reinterpret_cast<float*>(ws + g.off_part), reinterpret_cast<int*>(ws + g.off_done),
+                           static_cast<__nv_bfloat16*>(out), reinterpret_cast<WsHeader*>(ws), g, gq.split,
+                           1.0f / (alpha - 1.0f), 1.4426950408889634f / sqrtf((float)D));
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_decode_q8(const void* q, const void* kc, const void* vc, const void* ks, const void* vs,
                              const float* ksum, const int* kv_len, void* out, const DecodeQ8Geom& g, char* ws,
                              float alpha, float coarse_scale, cudaStream_t stream) {
     const int nctas = decode_tc_ctas();
-    cudaError_t e = launch_decode_lists(q, ksum, kv_len, out, g.real, g.v, ws, alpha, coarse_scale, nctas, stream, kQ8Per);
+    cudaError_t e = launch_decode_lists(q, ksum, kv_len, out, g.real, g.v, ws, alpha, coarse_scale, 0, stream, true);
     if (e != cudaSuccess) return e;
     return g.v.d == 128 ? launch_attn<128>(q, kc, vc, ks, vs, kv_len, out, g, ws, alpha, nctas, stream)
                         : launch_attn<64>(q, kc, vc, ks, vs, kv_len, out, g, ws, alpha, nctas, stream);

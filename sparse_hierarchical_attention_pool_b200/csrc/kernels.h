@@ -106,11 +106,12 @@ cudaError_t launch_cache_read(const void* kc, const void* vc, const void* ks, co
                               cudaStream_t stream);
 
 // scores, thresholds, block lists and work plan (for nctas CTAs, 0: none) of a decode step:
-// scores over the KV groups of g, lists over those of gl (g itself, or its virtual groups); at
-// least `per` list entries per CTA
+// scores over the KV groups of g, lists over those of gl (g itself, or its virtual groups).
+// pdl: the workspace header is cleared here and the kernels are chained by programmatic
+// dependent launch; otherwise the caller has cleared it.
 cudaError_t launch_decode_lists(const void* q, const float* ksum, const int* kv_len, void* out, const DecodeGeom& g,
                                 const DecodeGeom& gl, char* ws, float alpha, float coarse_scale, int nctas,
-                                cudaStream_t stream, int per = 1);
+                                cudaStream_t stream, bool pdl = false);
 
 // ---- decode step over the 8-bit cache
 cudaError_t launch_decode_q8(const void* q, const void* kc, const void* vc, const void* ks, const void* vs,

@@ -43,10 +43,13 @@ struct WarpRow {
         for (int k0 = 0; k0 * 32 < n; k0 += 32) {
             const int kn = min(32, (n - k0 * 32 + 31) / 32);
             unsigned mine = 0u;
-#pragma unroll 4
+#pragma unroll 8
             for (int k = 0; k < kn; ++k) {
                 const int j = (k0 + k) * 32 + lane;
-                const unsigned w = __ballot_sync(0xffffffffu, j < n && (j < ns ? s[j] : p[j]) > t);
+                float v = -INFINITY;
+                if (j < ns) v = s[j];
+                else if (j < n) v = p[j];
+                const unsigned w = __ballot_sync(0xffffffffu, v > t);
                 mine = lane == k ? w : mine;
             }
             bits += __popc(mine);
@@ -208,11 +211,6 @@ __device__ __forceinline__ float lane_start(const WarpRow& xr, float m, float al
     return alpha == 1.5f ? lane_start_t<1>(y, alpha) : alpha == 2.0f ? lane_start_t<2>(y, alpha) : lane_start_t<0>(y, alpha);
 }
 
-// Work plan of the balanced attention pass, built by the last select CTA to finish (a
-// ticket in the workspace header): offs = exclusive prefix of the list lengths (U = offs[BH]
-// blocks in all), and plan[c] = the group holding position floor(U c / n), where CTA c's
-// range starts (n = min(nctas, U)).  Called by every thread of every CTA once its count is
-// written.
 // CTAs that share U blocks: at most `grid`, and (per > 1) at least `per` blocks each where U
 // allows, so that short lists are not cut into pieces whose merge costs more than they save.
 __host__ __device__ inline int split_ctas(long long U, int grid, int per) {
@@ -220,8 +218,81 @@ __host__ __device__ inline int split_ctas(long long U, int grid, int per) {
     return (int)(n < (long long)grid ? n : (long long)grid);
 }
 
-static __device__ void decode_plan_tail(const int* count, int* offs, int* plan, WsHeader* hdr, int BH, int nctas,
-                                        int per = 1) {
+// A CTA's share of the concatenated lists, from their lengths alone: U entries in all, nC CTAs
+// with work, entries [lo, hi) for this one (empty for a CTA past nC), which begin in list
+// `first`, whose own first entry is o_first.  All NT threads of the CTA call it; sh: NT / 32 + 2 ints.
+struct ListShare {
+    int U, nC, lo, hi, first, o_first;
+};
+template <int NT>
+__device__ __forceinline__ ListShare list_share(const int* count, int lists, int cta, int grid, int per, int* sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int chunk = (lists + NT - 1) / NT, i0 = min(lists, tid * chunk), i1 = min(lists, i0 + chunk);
+    int sum = 0;
+#pragma unroll 4
+    for (int i = i0; i < i1; ++i) sum += __ldcg(count + i);
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) sh[warp] = incl;
+    __syncthreads();
+    int pre = incl - sum;
+    ListShare r;
+    r.U = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) pre += sh[w];
+        r.U += sh[w];
+    }
+    r.nC = split_ctas(r.U, grid, per);
+    r.lo = r.hi = 0;
+    if (cta < r.nC) {
+        r.lo = (int)((long long)r.U * cta / r.nC);
+        r.hi = (int)((long long)r.U * (cta + 1) / r.nC);
+    }
+    if (r.lo < r.hi && r.lo >= pre && r.lo < pre + sum) {
+        // one thread's lists hold the first entry
+        int i = i0, o = pre;
+        for (int c = __ldcg(count + i); o + c <= r.lo; c = __ldcg(count + i)) { o += c; ++i; }
+        sh[NT / 32] = i;
+        sh[NT / 32 + 1] = o;
+    }
+    __syncthreads();
+    r.first = sh[NT / 32];
+    r.o_first = sh[NT / 32 + 1];
+    return r;
+}
+
+// Programmatic dependent launch: a kernel that calls pdl_trigger lets its successor's blocks start
+// (launched with pdl_config) and run up to pdl_wait, which returns once every kernel before it
+// has finished and its writes are visible.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+struct PdlConfig {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    PdlConfig(dim3 grid, dim3 block, size_t smem, cudaStream_t stream) : cfg{} {
+        cfg.gridDim = grid;
+        cfg.blockDim = block;
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+};
+
+// Work plan of the balanced attention pass, built by the last select CTA to finish (a
+// ticket in the workspace header): offs = exclusive prefix of the list lengths (U = offs[BH]
+// blocks in all), and plan[c] = the group holding position floor(U c / n), where CTA c's
+// range starts (n = min(nctas, U)).  Called by every thread of every CTA once its count is
+// written.
+static __device__ void decode_plan_tail(const int* count, int* offs, int* plan, WsHeader* hdr, int BH, int nctas) {
     __shared__ int last_sh;
     __shared__ int wsum[32];
     __syncthreads();
@@ -246,7 +317,7 @@ static __device__ void decode_plan_tail(const int* count, int* offs, int* plan, 
         U += wsum[w];
     }
     if (threadIdx.x == 0) offs[BH] = U;
-    nctas = split_ctas(U, nctas, per);
+    nctas = split_ctas(U, nctas, 1);                  // the attention pass uses min(grid, U) CTAs
     for (int i0 = lo; i0 < hi; i0 += 32) {
         const int i = i0 + lane;
         const int v = i < hi ? __ldcg(count + i) : 0;

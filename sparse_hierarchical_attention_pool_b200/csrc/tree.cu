@@ -15,8 +15,7 @@
 // Kernels:
 //   1. tree_scores : x[row, j] = cx q . kbar_j for the full blocks on the tensor cores, and in one
 //                    CTA per KV group the ancestor masks, depths and the open block's scores;
-//   2. tree_select : thresholds (one warp per row), the union of every tile's selected blocks,
-//                    and the work plan;
+//   2. tree_select : thresholds (one warp per row) and the union of every tile's selected blocks;
 //   3. tree_attn, tree_combine (tree_tc.cu): every row over its selected blocks, the open block and
 //                    its path.
 #include "cache8.cuh"
@@ -100,6 +99,9 @@ tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
     __shared__ int par_s[kMaxNodes], dep_s[kMaxNodes];
     __shared__ float path[kMaxNodes][D], tail_s[D];
     const int bg = blockIdx.x, b = bg / g.Hkv, tid = threadIdx.x;
+    pdl_trigger();
+    if (bg == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid < (int)sizeof(WsHeader) / 16)
+        reinterpret_cast<uint4*>(w.hdr)[tid] = make_uint4(0u, 0u, 0u, 0u);
     int L, nodes;
     const bool live = tree_live(a.kv_len, a.n_nodes, g, b, &L, &nodes);
     const int F = live ? L / kBlock : 0;
@@ -195,7 +197,7 @@ tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
 constexpr int kTreeSelWarps = 8;
 
 __global__ void __launch_bounds__(kTreeSelWarps * 32)
-tree_select_kernel(TreeArgs a, TreeWork w, TreeGeom g, float alpha, float cx, int nctas, int per) {
+tree_select_kernel(TreeArgs a, TreeWork w, TreeGeom g, float alpha, float cx) {
     __shared__ int last_sh, list_sh[33 * kTreeSelWarps];
     extern __shared__ float rows_sm[];
     const int scap = min(g.cap, kSelCap);
@@ -208,6 +210,8 @@ tree_select_kernel(TreeArgs a, TreeWork w, TreeGeom g, float alpha, float cx, in
     int L, nodes;
     const bool live = tree_live(a.kv_len, a.n_nodes, g, b, &L, &nodes);
     const int F = live ? L / kBlock : 0, r = live ? L % kBlock : 0;
+    pdl_trigger();
+    pdl_wait();
     const int lrow = sub * kTreeSelWarps + warp;                     // row of the tile
     if (lrow < rows) {
         const size_t row = (size_t)bg * g.R + r0 + lrow;
@@ -270,7 +274,6 @@ tree_select_kernel(TreeArgs a, TreeWork w, TreeGeom g, float alpha, float cx, in
         }
     }
     if (tid == 0) w.count[tile] = total;
-    decode_plan_tail(w.count, w.offs, w.plan, w.hdr, g.tiles, nctas, per);
 }
 
 // ------------------------------------------------------------------ host side
@@ -296,9 +299,8 @@ static cudaError_t launch_tree_t(const TreeArgs& a, const TreeGeom& g, char* ws,
     const int sm = (g.cap < kSelCap ? g.cap : kSelCap) * kTreeSelWarps * (int)sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(tree_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
     if (e != cudaSuccess) return e;
-    tree_select_kernel<<<(unsigned)g.tiles * (kTreeRows / kTreeSelWarps), kTreeSelWarps * 32, sm, stream>>>(a, w, g, alpha, cx, nctas,
-                                                                                                      kTreePer);
-    e = cudaGetLastError();
+    const PdlConfig c((unsigned)g.tiles * (kTreeRows / kTreeSelWarps), kTreeSelWarps * 32, sm, stream);
+    e = cudaLaunchKernelEx(&c.cfg, tree_select_kernel, a, w, g, alpha, cx);
     if (e != cudaSuccess) return e;
     return launch_tree_attn(a, w, g, e_pow, sm2, nctas, kTreePer, stream);
 }

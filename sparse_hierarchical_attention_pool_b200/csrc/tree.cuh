@@ -16,7 +16,8 @@ struct TreeWork {
     int* depth;                          // [B][N]
     float* path;                         // [B Hkv][N][D] sum of the open block's keys on a node's path
     unsigned* bits;                      // [tile][nbw] selected blocks
-    int *tick, *list, *count, *offs, *plan;
+    int *tick, *list, *count;
+    int* offs;                           // [tile] first entry of split tiles; [tiles]: entries in all
     float* part;                         // [CTA + tile][128][max, sum, -, -, output D]
 };
 
@@ -33,7 +34,6 @@ inline TreeWork tree_work(const TreeGeom& g, char* ws) {
     w.list = reinterpret_cast<int*>(ws + g.off_list);
     w.count = reinterpret_cast<int*>(ws + g.off_count);
     w.offs = reinterpret_cast<int*>(ws + g.off_offs);
-    w.plan = reinterpret_cast<int*>(ws + g.off_plan);
     w.part = reinterpret_cast<float*>(ws + g.off_part);
     return w;
 }

@@ -58,8 +58,9 @@ struct TtLayout {
 
 // One 32-bit word of codes as four bf16, scaled: the code's exponent and mantissa bits moved to
 // bf16's place read as code 2^-120 (subnormals too), so two exact multiplications by powers of
-// two give code 2^(s - 127).
-__device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t w, __nv_bfloat162 f, uint32_t* lo, uint32_t* hi) {
+// two give code 2^(s - 127).  f2: 2^(s - 127) in both halves.
+__device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t w, uint32_t f2, uint32_t* lo, uint32_t* hi) {
+    const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&f2);
     const __nv_bfloat162 up = __floats2bfloat162_rn(0x1p120f, 0x1p120f);
     const uint32_t e = __byte_perm(w, 0u, 0x1404), o = __byte_perm(w, 0u, 0x3424);   // codes 0, 1 and 2, 3 in the high bytes
     const uint32_t a = (e & 0x80008000u) | ((e >> 4) & 0x07f007f0u), b = (o & 0x80008000u) | ((o >> 4) & 0x07f007f0u);
@@ -85,11 +86,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_sh;
     __shared__ float m_sh[2][kTreeRows];
-    const long long U = w.offs[g.tiles];
-    const int nC = split_ctas(U, (int)gridDim.x, per), cta = blockIdx.x;
-    if (cta >= nC) return;
-    const int r_lo = (int)(U * cta / nC), r_hi = (int)(U * (cta + 1) / nC);
-    const int tile_first = w.plan[cta];
+    constexpr int NT = Q8 ? 512 : 384;
+    __shared__ int share_sh[NT / 32 + 2];
+    const int cta = blockIdx.x;
 
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -115,22 +114,33 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         tmem_alloc(smem_u32(&tmem_sh), 512);
         tmem_relinquish();
     }
+    if constexpr (!Q8) {
+        if (warp == 8 && lane == 0) { prefetch_tmap(&tm_k); prefetch_tmap(&tm_kd); }
+        if (warp == 11 && lane == 0) { prefetch_tmap(&tm_v); prefetch_tmap(&tm_vd); }
+    }
     tc_fence_before();
-    __syncthreads();
+    pdl_trigger();
+    pdl_wait();
+    // its barriers also publish the set-up above
+    const ListShare sh = list_share<NT>(w.count, g.tiles, cta, (int)gridDim.x, per, share_sh);
     tc_fence_after();
+    const long long U = sh.U;
+    const int nC = sh.nC;
+    if (cta == 0 && tid == 0) w.offs[g.tiles] = sh.U;
     const uint32_t tmem = tmem_sh;
     volatile int* abort_flag = &abort_sh;
     auto k_addr = [&](int st) { return base + L::off_k + (uint32_t)st * L::kTile; };
     auto v_addr = [&](int st) { return base + L::off_v + (uint32_t)st * L::kTile; };
 
-    // calls body(tile, first entry, entries, step count before) for every segment of the range
+    // calls body(tile, first entry, entries, steps before, the tile's first entry in the
+    // concatenation, its end) for every segment of the range
     auto segments = [&](auto&& body) {
         int gs = 0;
-        for (int tile = tile_first, pos = r_lo; pos < r_hi; ++tile) {
-            const int o0 = w.offs[tile], o1 = w.offs[tile + 1];
+        for (int tile = sh.first, pos = sh.lo, o0 = sh.o_first, o1; pos < sh.hi; ++tile, o0 = o1) {
+            o1 = o0 + __ldcg(w.count + tile);
             if (o1 <= pos) continue;
-            const int n = min(r_hi, o1) - pos;
-            body(tile, pos - o0, n, gs);
+            const int n = min(sh.hi, o1) - pos;
+            body(tile, pos - o0, n, gs, o0, o1);
             pos += n;
             gs += n;
         }
@@ -141,8 +151,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (lane == 0) {
             bool ok = true;
             int armed = 0;                                       // steps loaded
-            if constexpr (!Q8) { prefetch_tmap(&tm_k); prefetch_tmap(&tm_kd); }
-            segments([&](int tile, int e0, int n, int gs) {
+            segments([&](int tile, int e0, int n, int gs, int, int) {
                 const int bg = tile / g.tiles_bg;
                 const int F = a.kv_len[bg / g.Hkv] / kBlock;
                 for (int s = 0; ok && s < n; ++s) {
@@ -189,8 +198,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             int special = 0, last_st[VS];
 #pragma unroll
             for (int i = 0; i < VS; ++i) last_st[i] = -1;
-            if (lane == 0) { prefetch_tmap(&tm_v); prefetch_tmap(&tm_vd); }
-            segments([&](int tile, int e0, int n, int gs) {
+            segments([&](int tile, int e0, int n, int gs, int, int) {
                 const int bg = tile / g.tiles_bg, b = bg / g.Hkv;
                 int len, nodes;
                 tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes);
@@ -246,7 +254,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const uint32_t idesc = idesc_bf16(128, 64, false);
             bool ok = true;
             int seg = 0;
-            segments([&](int, int, int n, int gs0) {
+            segments([&](int, int, int n, int gs0, int, int) {
                 if (ok && !mbar_wait(bar(B_Q), seg & 1, abort_flag)) ok = false;
                 ++seg;
                 for (int s = 0; ok && s < n; ++s) {
@@ -277,7 +285,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (lane == 0) {
             const uint32_t idesc_v = idesc_bf16(128, D, true), idesc_l = idesc_bf16(128, 16, false);
             bool ok = true;
-            segments([&](int, int, int n, int gs0) {
+            segments([&](int, int, int n, int gs0, int, int) {
                 for (int s = 0; ok && s < n; ++s) {
                     const int gs = gs0 + s, st = gs % VS, gp = gs & 1, i2 = gs >> 1, pb = kTtPBuf * gp + i2 % kTtPBuf;
                     if (!mbar_wait(bar(B_PF + pb), (i2 / kTtPBuf) & 1, abort_flag)) { ok = false; break; }
@@ -318,7 +326,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const auto* draft_rows = static_cast<const __nv_bfloat16*>(kv ? a.v_draft : a.k_draft);
             bool ok = true;
             int rs = 0;                                          // raw stages taken
-            segments([&](int tile, int e0, int n, int gs0) {
+            segments([&](int tile, int e0, int n, int gs0, int, int) {
                 const int bg = tile / g.tiles_bg, b = bg / g.Hkv;
                 int len, nodes;
                 tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes);
@@ -335,31 +343,60 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     if (!ok) continue;
                     const uint8_t* rp = base_ptr + L::off_raw + rst * L::kRaw;
                     uint8_t* dst = base_ptr + (kv ? L::off_v : L::off_k) + st * L::kTile;
-#pragma unroll 4
-                    for (int it = 0; it < kBlock * CH / 64; ++it) {
-                        const int idx = it * 64 + ct, r = idx / CH, c = idx % CH;
-                        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-                        if (r < lim) {
-                            if (draft) {
-                                const uint4* p = reinterpret_cast<const uint4*>(draft_rows + ((size_t)bg * g.N + r) * D) + c * 2;
-                                lo = __ldg(p);
-                                hi = __ldg(p + 1);
-                            } else {
-                                const uint4 x = *reinterpret_cast<const uint4*>(rp + kv * L::kRawKV + idx * 16);
-                                const float fs = scale_value(rp[2 * L::kRawKV + kv * 64 + r]);
-                                const __nv_bfloat162 f = __floats2bfloat162_rn(fs, fs);
-                                e4m3x4_to_bf16x4(x.x, f, &lo.x, &lo.y);
-                                e4m3x4_to_bf16x4(x.y, f, &lo.z, &lo.w);
-                                e4m3x4_to_bf16x4(x.z, f, &hi.x, &hi.y);
-                                e4m3x4_to_bf16x4(x.w, f, &hi.z, &hi.w);
-                            }
-                        }
-                        // chunks 2 c and 2 c + 1 of the row's half; the upper half's lanes store the
-                        // odd chunk first, so the lanes of a phase fall in distinct banks
-                        uint8_t* row = dst + (c >> 2) * L::kHalf + r * 128;
-                        const int c0 = (c & 3) * 2, sw = c >> 2;
+                    constexpr int IT = kBlock * CH / 64;
+                    // chunks 2 c and 2 c + 1 of a row's half; the upper half's lanes store the odd chunk
+                    // first, so the lanes of a phase fall in distinct banks
+                    const int c = ct % CH, sw = c >> 2, c0 = (c & 3) * 2;
+                    auto store = [&](int r, uint4 lo, uint4 hi) {
+                        uint8_t* row = dst + sw * L::kHalf + r * 128;
                         *reinterpret_cast<uint4*>(row + (((c0 + sw) ^ (r & 7)) << 4)) = sw ? hi : lo;
                         *reinterpret_cast<uint4*>(row + (((c0 + 1 - sw) ^ (r & 7)) << 4)) = sw ? lo : hi;
+                    };
+                    auto convert = [&](uint4 x, uint32_t sb, uint4* lo, uint4* hi) {
+                        const uint32_t f = sb == kScaleNaN ? 0x7fff7fffu : sb * 0x00800080u;   // 2^(s - 127), twice
+                        e4m3x4_to_bf16x4(x.x, f, &lo->x, &lo->y);
+                        e4m3x4_to_bf16x4(x.y, f, &lo->z, &lo->w);
+                        e4m3x4_to_bf16x4(x.z, f, &hi->x, &hi->y);
+                        e4m3x4_to_bf16x4(x.w, f, &hi->z, &hi->w);
+                    };
+                    const uint8_t* codes = rp + kv * L::kRawKV + ct * 16;
+                    const uint8_t* scales = rp + 2 * L::kRawKV + kv * 64 + ct / CH;
+                    constexpr int RS = 64 / CH;                  // rows per round of the 64 threads
+                    if (j >= 0) {
+                        constexpr int U4 = IT < 4 ? IT : 4;
+#pragma unroll 1
+                        for (int it0 = 0; it0 < IT; it0 += U4) {
+                            uint4 x[U4];
+                            uint32_t sb[U4];
+#pragma unroll
+                            for (int i = 0; i < U4; ++i) {
+                                x[i] = *reinterpret_cast<const uint4*>(codes + (it0 + i) * 1024);
+                                sb[i] = scales[(it0 + i) * RS];
+                            }
+#pragma unroll
+                            for (int i = 0; i < U4; ++i) {
+                                uint4 lo, hi;
+                                convert(x[i], sb[i], &lo, &hi);
+                                store((it0 + i) * RS + ct / CH, lo, hi);
+                            }
+                        }
+                    } else {
+                        // the open block's rows, or the draft's; zeros behind them
+#pragma unroll 1
+                        for (int it = 0; it < IT; ++it) {
+                            const int r = it * RS + ct / CH;
+                            uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+                            if (r < lim) {
+                                if (draft) {
+                                    const uint4* p = reinterpret_cast<const uint4*>(draft_rows + ((size_t)bg * g.N + r) * D) + c * 2;
+                                    lo = __ldg(p);
+                                    hi = __ldg(p + 1);
+                                } else {
+                                    convert(*reinterpret_cast<const uint4*>(codes + it * 1024), scales[it * RS], &lo, &hi);
+                                }
+                            }
+                            store(r, lo, hi);
+                        }
                     }
                     fence_proxy_async_smem();
                     mbar_arrive(bar(bF + st));
@@ -377,7 +414,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         auto wwait = [&](uint32_t bar_addr, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, abort_flag));
         };
-        segments([&](int tile, int e0, int n, int gs0) {
+        segments([&](int tile, int e0, int n, int gs0, int o0, int o1) {
             const int bg = tile / g.tiles_bg, b = bg / g.Hkv, row_g = (tile % g.tiles_bg) * kTreeRows + r;
             const bool in_tile = row_g < g.R;
             const size_t row = (size_t)bg * g.R + row_g;
@@ -518,6 +555,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 tc_fence_before();
                 mbar_arrive(bar(B_PF + kTtPBuf * grp + pb));
             }
+            if (tid == 0 && e0 == 0) w.offs[tile] = o0;          // for the merge of a split tile
             // ---- the two groups' states: (max, sum, output) of every row
             m_sh[grp][r] = m_run;
             asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -541,7 +579,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 const float l0 = __uint_as_float(tmem_ld1(lane_addr + L::colL)), l1 = __uint_as_float(tmem_ld1(lane_addr + L::colL + 16));
                 tmem_wait_ld();
                 const float den = (w0 > 0.f ? l0 * w0 : 0.f) + (w1 > 0.f ? l1 * w1 : 0.f);
-                const int o0 = w.offs[tile], o1 = w.offs[tile + 1];
                 const bool direct = dt_cta_of(o0, U, nC) == dt_cta_of(o1 - 1, U, nC);
                 float* pr = w.part + (((size_t)cta + tile) * kTreeRows + r) * (D + 4);
                 if (!direct && valid && grp == 0) { pr[0] = M; pr[1] = den; }
@@ -602,9 +639,11 @@ tree_combine_kernel(TreeArgs a, TreeWork w, TreeGeom g, int nctas, int per) {
     const int tile = blockIdx.x / kPerTile, r = (blockIdx.x % kPerTile) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int bg = tile / g.tiles_bg, b = bg / g.Hkv, row_g = (tile % g.tiles_bg) * kTreeRows + r;
     if (row_g >= g.R) return;
+    pdl_wait();
+    const int n = w.count[tile];
+    if (n == 0) return;
     const long long U = w.offs[g.tiles];
-    const int o0 = w.offs[tile], o1 = w.offs[tile + 1];
-    if (o1 == o0) return;
+    const int o0 = w.offs[tile], o1 = o0 + n;
     const int nC = split_ctas(U, nctas, per);
     const int c0 = dt_cta_of(o0, U, nC), c1 = dt_cta_of(o1 - 1, U, nC);
     if (c0 == c1) return;
@@ -630,15 +669,26 @@ tree_combine_kernel(TreeArgs a, TreeWork w, TreeGeom g, int nctas, int per) {
             den = fmaf(ml.y, wt, den);
         }
         const int kn = min(32, np - i0);
-#pragma unroll 8
-        for (int k = 0; k < kn; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, wt, k);
-            const float* pi = p + (i0 + k) * step + 4 + lane * DPL;
+        constexpr int KB = 8;                          // pieces whose loads are in flight together
+        for (int k0 = 0; k0 < kn; k0 += KB) {
+            float v[KB][DPL];
 #pragma unroll
-            for (int d = 0; d < DPL / 2; ++d) {
-                const float2 t = __ldcg(reinterpret_cast<const float2*>(pi) + d);
-                num[2 * d] = fmaf(t.x, wk, num[2 * d]);
-                num[2 * d + 1] = fmaf(t.y, wk, num[2 * d + 1]);
+            for (int k = 0; k < KB; ++k) {
+                // past the last piece: that piece again, with weight 0
+                const float* pi = p + (i0 + min(k0 + k, kn - 1)) * step + 4 + lane * DPL;
+                if constexpr (DPL == 4) {
+                    const float4 t = __ldcg(reinterpret_cast<const float4*>(pi));
+                    v[k][0] = t.x; v[k][1] = t.y; v[k][2] = t.z; v[k][3] = t.w;
+                } else {
+                    const float2 t = __ldcg(reinterpret_cast<const float2*>(pi));
+                    v[k][0] = t.x; v[k][1] = t.y;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < KB; ++k) {
+                const float wk = k0 + k < kn ? __shfl_sync(0xffffffffu, wt, k0 + k) : 0.f;
+#pragma unroll
+                for (int d = 0; d < DPL; ++d) num[d] = fmaf(v[k][d], wk, num[d]);
             }
         }
     }
@@ -662,11 +712,12 @@ static cudaError_t launch_t(const TreeArgs& a, const TreeWork& w, const TreeGeom
     const int sm = (int)TtLayout<D, Q8>::bytes;
     cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
     if (e != cudaSuccess) return e;
-    tree_attn_kernel<D, Q8><<<nctas, Q8 ? 512 : 384, sm, stream>>>(tk, tv, tkd, tvd, a, w, g, e_pow, sm2, per);
-    e = cudaGetLastError();
+    const PdlConfig ca(nctas, Q8 ? 512 : 384, sm, stream);
+    e = cudaLaunchKernelEx(&ca.cfg, tree_attn_kernel<D, Q8>, tk, tv, tkd, tvd, a, w, g, e_pow, sm2, per);
     if (e != cudaSuccess) return e;
-    tree_combine_kernel<D><<<(unsigned)g.tiles * (kTreeRows / 8), 256, 0, stream>>>(a, w, g, nctas, per);
-    return cudaGetLastError();
+    const PdlConfig cc((unsigned)g.tiles * (kTreeRows / 8), 256, 0, stream);
+    e = cudaLaunchKernelEx(&cc.cfg, tree_combine_kernel<D>, a, w, g, nctas, per);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_tree_attn(const TreeArgs& a, const TreeWork& w, const TreeGeom& g, float e_pow, float sm2, int nctas,
