@@ -208,7 +208,7 @@ inline bool make_decode_q8_geom(int B, int Hq, int Hkv, int Tmax, int d, DecodeQ
     while (g->real.G % g->split != 0 || g->real.G / g->split > 8) ++g->split;
     if (!make_decode_geom(B, Hq, Hkv * g->split, Tmax, d, &g->v)) return false;
     // partials hold two maxima and the sum (16 bytes with padding) and the output per head
-    const size_t slots = (size_t)B * Hkv * g->split + kDecodeMaxCtas;
+    const size_t slots = ((size_t)B * Hkv * g->split + kDecodeMaxCtas) * 4;      // one per consumer warp
     g->v.total = align256(g->v.off_part + slots * g->v.G * (d + 4) * sizeof(float));
     return true;
 }

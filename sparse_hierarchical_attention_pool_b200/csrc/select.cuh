@@ -266,6 +266,35 @@ __device__ __forceinline__ ListShare list_share(const int* count, int lists, int
     return r;
 }
 
+// A warp's walk along list entries [e, end): 64 of them in registers, so that a producer neither
+// waits for one entry's load before each copy nor reads ahead one by one.  at(e + k) for
+// k < 32 from the current entry e; every lane calls it.
+struct ListWindow {
+    const int* p;
+    int base, end, cur, nxt;
+    __device__ __forceinline__ int fetch(int e) const {
+        const int i = e + (threadIdx.x & 31);
+        return i < end ? __ldcg(p + i) : 0;
+    }
+    __device__ __forceinline__ void start(const int* list, int e, int e_end) {
+        p = list; base = e; end = e_end;
+        cur = fetch(e);
+        nxt = fetch(e + 32);
+    }
+    // the entry is now e (called with e increasing by one)
+    __device__ __forceinline__ void to(int e) {
+        if (e - base == 32) {
+            base = e;
+            cur = nxt;
+            nxt = fetch(e + 32);
+        }
+    }
+    __device__ __forceinline__ int at(int e) const {
+        const int k = e - base;
+        return __shfl_sync(0xffffffffu, k < 32 ? cur : nxt, k & 31);
+    }
+};
+
 // Programmatic dependent launch: a kernel that calls pdl_trigger lets its successor's blocks start
 // (launched with pdl_config) and run up to pdl_wait, which returns once every kernel before it
 // has finished and its writes are visible.

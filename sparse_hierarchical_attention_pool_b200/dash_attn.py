@@ -589,9 +589,11 @@ def dash_cache_read(k_cache, v_cache, k_scale, v_scale, n, start=None, kv_len=No
     behind kv_len[b] are zero.  start, kv_len int32 [B] (None: 0 and Tmax)."""
     B, Hkv, Tmax, d = k_cache.shape
     dev, full, flat, rows = k_cache.get_device(), (B, Hkv, Tmax, d), (B, Hkv, Tmax), (B, Hkv, n, d)
-    if k_out is None:
+    if k_out is None and v_out is None:
+        k_out, v_out = torch.empty((2, *rows), dtype=torch.bfloat16, device=k_cache.device).unbind()
+    elif k_out is None:
         k_out = torch.empty(rows, dtype=torch.bfloat16, device=k_cache.device)
-    if v_out is None:
+    elif v_out is None:
         v_out = torch.empty(rows, dtype=torch.bfloat16, device=k_cache.device)
     args = (_ptr(k_cache, _E4M3, full, dev, "k_cache"), _ptr(v_cache, _E4M3, full, dev, "v_cache"),
             _ptr(k_scale, _U8, flat, dev, "k_scale"), _ptr(v_scale, _U8, flat, dev, "v_scale"),
