@@ -101,7 +101,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[kQ8Stages], empty[kQ8Stages];
     __shared__ int abort_sh;
-    __shared__ int share_sh[kQ8Warps + 3];
+    __shared__ int share_sh[kQ8Warps + 4];
     const int cap = g.nbs + 1, cta = blockIdx.x;
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -136,7 +136,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         long long cnt = 0;
         bool ok = true;
         for (int bg = sh.first, pos = sh.lo, o0 = sh.o_first, o1; ok && pos < sh.hi; ++bg, o0 = o1) {
-            o1 = o0 + __ldcg(count + bg);
+            o1 = bg == sh.first ? sh.o_end : o0 + __ldcg(count + bg);
             if (o1 <= pos) continue;
             const int e_end = min(sh.hi, o1) - o0;
             if (pos == o0 && lane == 0) offs[bg] = o0;

@@ -220,17 +220,21 @@ __host__ __device__ inline int split_ctas(long long U, int grid, int per) {
 
 // A CTA's share of the concatenated lists, from their lengths alone: U entries in all, nC CTAs
 // with work, entries [lo, hi) for this one (empty for a CTA past nC), which begin in list
-// `first`, whose own first entry is o_first.  All NT threads of the CTA call it; sh: NT / 32 + 2 ints.
+// `first`, whose own entries are [o_first, o_end).  All NT threads of the CTA call it; sh: NT / 32 + 3 ints.
 struct ListShare {
-    int U, nC, lo, hi, first, o_first;
+    int U, nC, lo, hi, first, o_first, o_end;
 };
 template <int NT>
 __device__ __forceinline__ ListShare list_share(const int* count, int lists, int cta, int grid, int per, int* sh) {
+    constexpr int KEEP = 4;                            // lengths a thread keeps
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int chunk = (lists + NT - 1) / NT, i0 = min(lists, tid * chunk), i1 = min(lists, i0 + chunk);
-    int sum = 0;
-#pragma unroll 4
-    for (int i = i0; i < i1; ++i) sum += __ldcg(count + i);
+    int c[KEEP], sum = 0;
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k) c[k] = i0 + k < i1 ? __ldcg(count + i0 + k) : 0;
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k) sum += c[k];
+    for (int i = i0 + KEEP; i < i1; ++i) sum += __ldcg(count + i);
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -255,14 +259,22 @@ __device__ __forceinline__ ListShare list_share(const int* count, int lists, int
     }
     if (r.lo < r.hi && r.lo >= pre && r.lo < pre + sum) {
         // one thread's lists hold the first entry
-        int i = i0, o = pre;
-        for (int c = __ldcg(count + i); o + c <= r.lo; c = __ldcg(count + i)) { o += c; ++i; }
+        int i = i0, o = pre, n = 0;
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k)
+            if (i == i0 + k && i < i1) {
+                n = c[k];
+                if (o + n <= r.lo) { o += n; ++i; }
+            }
+        for (; i >= i0 + KEEP && (n = __ldcg(count + i), o + n <= r.lo); ++i) o += n;
         sh[NT / 32] = i;
         sh[NT / 32 + 1] = o;
+        sh[NT / 32 + 2] = o + n;
     }
     __syncthreads();
     r.first = sh[NT / 32];
     r.o_first = sh[NT / 32 + 1];
+    r.o_end = sh[NT / 32 + 2];
     return r;
 }
 
@@ -296,7 +308,7 @@ struct ListWindow {
 };
 
 // Programmatic dependent launch: a kernel that calls pdl_trigger lets its successor's blocks start
-// (launched with pdl_config) and run up to pdl_wait, which returns once every kernel before it
+// (launched with PdlConfig) and run up to pdl_wait, which returns once every kernel before it
 // has finished and its writes are visible.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -18,7 +18,7 @@ struct TreeWork {
     unsigned* bits;                      // [tile][nbw] selected blocks
     int *tick, *list, *count;
     int* offs;                           // [tile] first entry of split tiles; [tiles]: entries in all
-    float* part;                         // [CTA + tile][128][max, sum, -, -, output D]
+    float* part;                         // [CTA + tile] partials of 128 rows (tree_tc.cu)
 };
 
 inline TreeWork tree_work(const TreeGeom& g, char* ws) {

@@ -2,25 +2,27 @@
 // lists of the tiles (tree.cu: what a list holds).
 //
 // A tile is up to 128 rows (heads x nodes) of one KV group and the M rows of both products:
-// S = Q K^T (N = 64 keys) into TMEM, softmax weights P in bf16 through shared memory, O += P V
-// and the row sums L += P 1 in TMEM.  The tensor core does 128 rows at the price of one, so
-// rows that a tile lacks cost no time; what bounds the kernel is the K/V stream (each list
-// entry's 64 rows once per tile) and, per step, one row's chain S -> weights -> P.
+// S = Q K^T (N = 64 keys) into TMEM, softmax weights P back into TMEM, O += P V in TMEM.  The
+// tensor core does 128 rows at the price of one, so rows that a tile lacks cost no time.  Q and P
+// are A operands in TMEM: with both in shared memory its 128 bytes a cycle were what bounded
+// a step (80 KB of operands and 48 KB of writes; now 32 KB and 32 KB), not HBM.
 //
-// Work split as in decode_tc.cu: the lists laid end to end hold U entries, CTA c of n takes
+// Work split as in decode_q8.cu: the lists laid end to end hold U entries, CTA c of n takes
 // entries [U c / n, U (c + 1) / n); a tile inside one CTA is finished there, the others leave
 // (max, sum, output) per row in slot CTA + tile for tree_combine_kernel.
 //
 // Roles (warps): 0 - 7 softmax, two groups of 128 threads (one per row) that take the steps
-// alternately, each with its own S, P buffers, O, row sum and maximum, merged at the end of a
-// segment; 8 K producer; 9 issuer of S; 10 issuer of P V; 11 V producer.  Counters of rings and
-// barriers run over the CTA's whole range; only the Q tile and the accumulators belong to a
-// segment.  The value rows that no row may attend (the open block's behind the sequence, the
-// draft's behind its nodes) are overwritten with zeros before the product: weight 0 times
-// whatever they hold would not be 0 if that were NaN.
-// 8-bit cache: warp 8 streams codes and scale bytes with bulk copies into a ring of their own,
-// and warps 12, 13 (K) and 14, 15 (V) turn them into the bf16 operand tiles (exact: cache8.cuh) or load the
-// draft's bf16 rows.
+// alternately, each with its own S, P, O, sum and maximum, merged at the end of a segment;
+// 8 K producer; 9 issuer of S; 10 issuer of P V; 11 V producer.  Counters of rings and barriers
+// run over the CTA's whole range; only Q and the accumulators belong to a segment.  The value rows
+// that no row may attend (the open block's behind the sequence, the draft's behind its nodes)
+// are zeros in the product: weight 0 times whatever they hold would not be 0 if that were NaN.
+//
+// 8-bit cache: warp 8 streams codes and scale bytes with bulk copies into a ring of their own, and
+// warps 12 - 15 (K) and 16 - 19 (V) turn them into bf16 operand tiles (exact: cache8.cuh) or load
+// the draft's bf16 rows.  Two warps a tensor convert too slowly (32K, 8 x 16 nodes: 112 us a step
+// against 98); tiles of f16 codes with the scales outside the product save conversions but need
+// another factor per step in every role, and measured 115.
 // Every wait is bounded; a CTA that gives up sets a status bit.
 #include "cache8.cuh"
 #include "kernels.h"
@@ -30,30 +32,28 @@
 
 namespace dash {
 
-constexpr int kTtK = 2, kTtV = 2;      // operand tile rings of the 8-bit variant
-constexpr int kTtPBuf = 2;             // P buffers per group
-constexpr int kTtRaw = 3;              // 8-bit ring
+constexpr int kTtRaw = 6;              // 8-bit ring
+constexpr int kTtConv = 4;             // converter warps for K, and for V
+template <bool Q8>
+constexpr int kTtThreads = Q8 ? 384 + kTtConv * 64 : 384;
 constexpr float kTtLazy = 8.0f;        // log2 units a maximum may grow before O is rescaled
 
 template <int D, bool Q8>
 struct TtLayout {
-    static constexpr int kKS = Q8 ? kTtK : 3, kVS = Q8 ? kTtV : 3;
-    static constexpr uint32_t kHalf = 64 * 128;                 // 64 rows x 64 bf16
+    static constexpr int kKS = Q8 ? 2 : 5, kVS = Q8 ? 3 : 5;    // operand tile rings
+    static constexpr uint32_t kHalf = 64 * 128;                 // 64 rows x 64 elements
     static constexpr uint32_t kTile = (D / 64) * kHalf;         // K or V of one entry
-    static constexpr uint32_t kQHalf = 128 * 128;
-    static constexpr uint32_t kP = 128 * 128;
     static constexpr uint32_t kRawKV = 64 * D;                  // codes of K or V of one entry
     static constexpr uint32_t kRaw = 2 * kRawKV + 128;          // and the scale bytes
-    static constexpr uint32_t off_q = 0;
-    static constexpr uint32_t off_k = (D / 64) * kQHalf;
+    static constexpr uint32_t off_k = 0;
     static constexpr uint32_t off_v = off_k + kKS * kTile;
-    static constexpr uint32_t off_p = off_v + kVS * kTile;
-    static constexpr uint32_t off_ones = off_p + 2 * kTtPBuf * kP;
-    static constexpr uint32_t off_raw = off_ones + 2048;
-    static constexpr uint32_t bytes = off_raw + (Q8 ? kTtRaw * kRaw : 0) + 1024;
+    static constexpr uint32_t off_raw = off_v + kVS * kTile;
+    static constexpr uint32_t used = off_raw + (Q8 ? kTtRaw * kRaw : 0) + 1024;
+    // more than half an SM's shared memory: the CTA's 512 TMEM columns are all there are
+    static constexpr uint32_t bytes = used > 120 * 1024 ? used : 120 * 1024;
     static_assert(bytes + 4096 <= 227 * 1024, "shared memory of one CTA per SM");
-    // TMEM columns: S of group g at 64 g, O at 128 + D g, row sums at 384 + 16 g
-    static constexpr uint32_t colO = 128, colL = 384;
+    // TMEM columns: S of group g at 64 g, O at 128 + D g, Q (two 16-bit elements a column), P of group g
+    static constexpr uint32_t colO = 128, colQ = 384, colP = 448;
 };
 
 // One 32-bit word of codes as four bf16, scaled: the code's exponent and mantissa bits moved to
@@ -71,7 +71,7 @@ __device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t w, uint32_t f2, uint32
 }
 
 template <int D, bool Q8>
-__global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
+__global__ void __launch_bounds__(kTtThreads<Q8>, 1)
 tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ CUtensorMap tm_kd, const __grid_constant__ CUtensorMap tm_vd, TreeArgs a,
                  TreeWork w, TreeGeom g, float e_pow, float sm2, int per) {
@@ -79,15 +79,15 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     using namespace sm100;
     constexpr int KS = L::kKS, VS = L::kVS;
     enum : int { B_Q = 0, B_KF = 1, B_KE = B_KF + KS, B_VF = B_KE + KS, B_VE = B_VF + VS, B_SF = B_VE + VS, B_SE = B_SF + 2,
-                 B_PF = B_SE + 2, B_PD = B_PF + 2 * kTtPBuf, B_RF = B_PD + 2 * kTtPBuf, B_RE = B_RF + kTtRaw,
+                 B_PF = B_SE + 2, B_PD = B_PF + 2, B_RF = B_PD + 2, B_RE = B_RF + kTtRaw,
                  B_VT = B_RE + kTtRaw, B_DR = B_VT + 1, B_COUNT = B_DR + 2 };
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[B_COUNT];
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_sh;
-    __shared__ float m_sh[2][kTreeRows];
-    constexpr int NT = Q8 ? 512 : 384;
-    __shared__ int share_sh[NT / 32 + 2];
+    __shared__ float m_sh[2][kTreeRows], l_sh[2][kTreeRows];     // the groups' maxima and sums
+    constexpr int NT = kTtThreads<Q8>;
+    __shared__ int share_sh[NT / 32 + 3];
     const int cta = blockIdx.x;
 
     const uint32_t raw = smem_u32(smem_raw);
@@ -98,18 +98,21 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const auto* q = static_cast<const __nv_bfloat16*>(a.q);
     if (tid == 0) {
         abort_sh = 0;
-        const int conv = Q8 ? 64 : 1;                           // who fills an operand tile
-        mbar_init(bar(B_Q), 256);
+        const int conv = Q8 ? kTtConv * 32 : 1;                          // who fills an operand tile
+        mbar_init(bar(B_Q), 128);
         for (int i = 0; i < KS; ++i) { mbar_init(bar(B_KF + i), conv); mbar_init(bar(B_KE + i), 1); }
         for (int i = 0; i < VS; ++i) { mbar_init(bar(B_VF + i), conv); mbar_init(bar(B_VE + i), 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(bar(B_SF + i), 1); mbar_init(bar(B_SE + i), 128); mbar_init(bar(B_DR + i), 1); }
-        for (int i = 0; i < 2 * kTtPBuf; ++i) { mbar_init(bar(B_PF + i), 128); mbar_init(bar(B_PD + i), 1); }
-        for (int i = 0; i < kTtRaw; ++i) { mbar_init(bar(B_RF + i), 1); mbar_init(bar(B_RE + i), 128); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_SF + i), 1);
+            mbar_init(bar(B_SE + i), 128);
+            mbar_init(bar(B_PF + i), 128);
+            mbar_init(bar(B_PD + i), 1);
+            mbar_init(bar(B_DR + i), 1);
+        }
+        for (int i = 0; i < kTtRaw; ++i) { mbar_init(bar(B_RF + i), 1); mbar_init(bar(B_RE + i), kTtConv * 64); }
         mbar_init(bar(B_VT), 1);
         fence_mbar_init();
     }
-    if (tid < 128) reinterpret_cast<uint4*>(base_ptr + L::off_ones)[tid] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-    fence_proxy_async_smem();
     if (warp == 0) {
         tmem_alloc(smem_u32(&tmem_sh), 512);
         tmem_relinquish();
@@ -137,7 +140,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     auto segments = [&](auto&& body) {
         int gs = 0;
         for (int tile = sh.first, pos = sh.lo, o0 = sh.o_first, o1; pos < sh.hi; ++tile, o0 = o1) {
-            o1 = o0 + __ldcg(w.count + tile);
+            o1 = tile == sh.first ? sh.o_end : o0 + __ldcg(w.count + tile);
             if (o1 <= pos) continue;
             const int n = min(sh.hi, o1) - pos;
             body(tile, pos - o0, n, gs, o0, o1);
@@ -146,20 +149,29 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
     };
 
+    // Q8: 640 threads have 96 registers each; the softmax's 64 scores a thread want more, the others less
+    // (256 x 136 + 128 x 56 + 256 x 72 = 60,416 of the 61,440 the block holds)
+    if (warp >= 8 && warp < 12) {
+        if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
     if (warp == 8) {
         // ------------------------------------------------------------ K producer / 8-bit stream
-        if (lane == 0) {
-            bool ok = true;
-            int armed = 0;                                       // steps loaded
-            segments([&](int tile, int e0, int n, int gs, int, int) {
-                const int bg = tile / g.tiles_bg;
-                const int F = a.kv_len[bg / g.Hkv] / kBlock;
-                for (int s = 0; ok && s < n; ++s) {
-                    const int j = w.list[(size_t)tile * g.lcap + e0 + s];
-                    if constexpr (Q8) {
-                        if (j == kTreeDraft) continue;           // loaded by the converters
-                        const int st = armed % kTtRaw;
-                        if (armed >= kTtRaw && !mbar_wait(bar(B_RE + st), ((armed / kTtRaw) - 1) & 1, abort_flag)) { ok = false; break; }
+        // one lane copies, the warp walks the list
+        bool ok = true;
+        int armed = 0;                                           // steps loaded
+        segments([&](int tile, int e0, int n, int gs, int, int) {
+            const int bg = tile / g.tiles_bg;
+            const int F = a.kv_len[bg / g.Hkv] / kBlock;
+            ListWindow win;
+            win.start(w.list + (size_t)tile * g.lcap, e0, e0 + n);
+            for (int s = 0; ok && s < n; ++s) {
+                win.to(e0 + s);
+                const int j = win.at(e0 + s);
+                if constexpr (Q8) {
+                    if (j == kTreeDraft) continue;               // loaded by the converters
+                    const int st = armed % kTtRaw;
+                    const bool got = armed < kTtRaw || mbar_wait(bar(B_RE + st), ((armed / kTtRaw) - 1) & 1, abort_flag);
+                    if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                    if (lane == 0) {
                         const size_t row = (size_t)bg * g.Tmax + (size_t)(j == kTreeOpen ? F : j) * kBlock;
                         const uint32_t dst = base + L::off_raw + (uint32_t)st * L::kRaw, bf = bar(B_RF + st);
                         mbar_arrive_expect_tx(bf, L::kRaw);
@@ -167,28 +179,31 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         bulk_load_1d(dst + L::kRawKV, static_cast<const uint8_t*>(a.v_cache) + row * D, L::kRawKV, bf);
                         bulk_load_1d(dst + 2 * L::kRawKV, static_cast<const uint8_t*>(a.k_scale) + row, 64, bf);
                         bulk_load_1d(dst + 2 * L::kRawKV + 64, static_cast<const uint8_t*>(a.v_scale) + row, 64, bf);
-                    } else {
-                        const int st = (gs + s) % KS;
-                        if (gs + s >= KS && !mbar_wait(bar(B_KE + st), (((gs + s) / KS) - 1) & 1, abort_flag)) { ok = false; break; }
+                    }
+                } else {
+                    const int st = (gs + s) % KS;
+                    const bool got = gs + s < KS || mbar_wait(bar(B_KE + st), (((gs + s) / KS) - 1) & 1, abort_flag);
+                    if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                    if (lane == 0) {
                         mbar_arrive_expect_tx(bar(B_KF + st), L::kTile);
                         const CUtensorMap* tm = j == kTreeDraft ? &tm_kd : &tm_k;
                         const int row = j == kTreeDraft ? bg * g.N : bg * g.Tmax + (j == kTreeOpen ? F : j) * kBlock;
 #pragma unroll
                         for (int h = 0; h < D / 64; ++h) tma_load_2d(k_addr(st) + h * L::kHalf, tm, h * 64, row, bar(B_KF + st));
                     }
-                    ++armed;
                 }
-            });
-            if (!ok) {
-                // every load this thread started lands before the CTA exits
-                constexpr int NS = Q8 ? kTtRaw : KS;
-                volatile int dummy = 0;
-                for (int st = 0; st < NS; ++st) {
-                    if (armed <= st) continue;
-                    const int last = armed - 1 - ((armed - 1 - st) % NS);
-                    dummy = 0;
-                    mbar_wait(bar((Q8 ? (int)B_RF : (int)B_KF) + st), (last / NS) & 1, &dummy);
-                }
+                ++armed;
+            }
+        });
+        if (!ok && lane == 0) {
+            // every load this thread started lands before the CTA exits
+            constexpr int NS = Q8 ? kTtRaw : KS;
+            volatile int dummy = 0;
+            for (int st = 0; st < NS; ++st) {
+                if (armed <= st) continue;
+                const int last = armed - 1 - ((armed - 1 - st) % NS);
+                dummy = 0;
+                mbar_wait(bar((Q8 ? (int)B_RF : (int)B_KF) + st), (last / NS) & 1, &dummy);
             }
         }
     } else if (warp == 11) {
@@ -203,8 +218,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 int len, nodes;
                 tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes);
                 const int F = len / kBlock;
+                ListWindow win;
+                win.start(w.list + (size_t)tile * g.lcap, e0, e0 + n);
                 for (int s = 0; ok && s < n; ++s) {
-                    const int j = w.list[(size_t)tile * g.lcap + e0 + s];
+                    win.to(e0 + s);
+                    const int j = win.at(e0 + s);
                     const int st = (gs + s) % VS;
                     bool got = gs + s < VS || mbar_wait(bar(B_VE + st), (((gs + s) / VS) - 1) & 1, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
@@ -252,6 +270,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         // ------------------------------------------------------------ S issuer
         if (lane == 0) {
             const uint32_t idesc = idesc_bf16(128, 64, false);
+            // descriptors are linear in the address (its bits fit the field)
+            const uint64_t dk0 = smem_desc_sw128(base + L::off_k, 16, 1024);
             bool ok = true;
             int seg = 0;
             segments([&](int, int, int n, int gs0, int, int) {
@@ -261,15 +281,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     const int gs = gs0 + s, st = gs % KS, sb = gs & 1, i2 = gs >> 1;
                     if (!mbar_wait(bar(B_KF + st), (gs / KS) & 1, abort_flag)) { ok = false; break; }
                     if (i2 >= 1 && !mbar_wait(bar(B_SE + sb), (i2 - 1) & 1, abort_flag)) { ok = false; break; }
-                    // a group that sees this S may write its P buffer: the buffer's last product has landed
-                    if (i2 >= kTtPBuf && !mbar_wait(bar(B_PD + kTtPBuf * sb + i2 % kTtPBuf), ((i2 - kTtPBuf) / kTtPBuf) & 1, abort_flag)) { ok = false; break; }
                     tc_fence_after();
+                    const uint64_t dk = dk0 + (uint32_t)st * (L::kTile >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t da = smem_desc_sw128(base + L::off_q + (kk >> 2) * L::kQHalf + (kk & 3) * 32, 16, 1024);
-                        const uint64_t db = smem_desc_sw128(k_addr(st) + (kk >> 2) * L::kHalf + (kk & 3) * 32, 16, 1024);
-                        mma_bf16_ss(tmem + sb * 64, da, db, idesc, kk > 0 ? 1u : 0u);
-                    }
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_bf16_ts(tmem + sb * 64, tmem + L::colQ + kk * 8, dk + (kk >> 2) * (L::kHalf >> 4) + (kk & 3) * 2, idesc, kk > 0 ? 1u : 0u);
                     mma_commit(bar(B_SF + sb));
                     mma_commit(bar(B_KE + st));
                 }
@@ -283,29 +299,21 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     } else if (warp == 10) {
         // ------------------------------------------------------------ PV issuer
         if (lane == 0) {
-            const uint32_t idesc_v = idesc_bf16(128, D, true), idesc_l = idesc_bf16(128, 16, false);
+            const uint32_t idesc_v = idesc_bf16(128, D, true);
+            const uint64_t dv0 = smem_desc_sw128(base + L::off_v, L::kHalf, 1024);
             bool ok = true;
             segments([&](int, int, int n, int gs0, int, int) {
                 for (int s = 0; ok && s < n; ++s) {
-                    const int gs = gs0 + s, st = gs % VS, gp = gs & 1, i2 = gs >> 1, pb = kTtPBuf * gp + i2 % kTtPBuf;
-                    if (!mbar_wait(bar(B_PF + pb), (i2 / kTtPBuf) & 1, abort_flag)) { ok = false; break; }
+                    const int gs = gs0 + s, st = gs % VS, gp = gs & 1, i2 = gs >> 1;
                     if (!mbar_wait(bar(B_VF + st), (gs / VS) & 1, abort_flag)) { ok = false; break; }
+                    if (!mbar_wait(bar(B_PF + gp), i2 & 1, abort_flag)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t acc = s >= 2 ? 1u : 0u;       // a group's first step of the segment overwrites
-                    const uint32_t pa = base + L::off_p + pb * L::kP;
+                    const uint64_t dv = dv0 + (uint32_t)st * (L::kTile >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t da = smem_desc_sw128(pa + kk * 32, 16, 1024);
-                        const uint64_t dv = smem_desc_sw128(v_addr(st) + kk * 2048, L::kHalf, 1024);
-                        mma_bf16_ss(tmem + L::colO + gp * D, da, dv, idesc_v, (acc || kk > 0) ? 1u : 0u);
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t da = smem_desc_sw128(pa + kk * 32, 16, 1024);
-                        const uint64_t d1 = smem_desc_sw128(base + L::off_ones + kk * 32, 16, 1024);
-                        mma_bf16_ss(tmem + L::colL + gp * 16, da, d1, idesc_l, (acc || kk > 0) ? 1u : 0u);
-                    }
-                    mma_commit(bar(B_PD + pb));
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16_ts(tmem + L::colO + gp * D, tmem + L::colP + gp * 32 + kk * 8, dv + kk * 128, idesc_v, (acc || kk > 0) ? 1u : 0u);
+                    mma_commit(bar(B_PD + gp));
                     mma_commit(bar(B_VE + st));
                 }
             });
@@ -315,13 +323,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 mbar_wait(bar(B_DR + 1), 0, &dummy);
             }
         }
+    }
     } else if (warp >= 12) {
+        if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
         // ------------------------------------------------------------ converters (8-bit cache)
         if constexpr (Q8) {
-            // two warps for K and two for V, each pair at its own ring's pace: V tiles are free
-            // only after their product, K tiles long before
-            constexpr int CH = D / 16, NS = kTtK;                // 16-code chunks per row
-            const int kv = (warp - 12) >> 1, ct = tid & 63;
+            // warps for K and warps for V, each at its own ring's pace: V tiles are free only
+            // after their product, K tiles long before
+            constexpr int CH = D / 16;                           // 16-code chunks per row
+            const int kv = (warp - 12) / kTtConv, ct = (tid - 384) % (kTtConv * 32), NS = kv ? VS : KS;
+            constexpr int CT = kTtConv * 32;                     // threads of a tensor
             const int bF = kv ? (int)B_VF : (int)B_KF, bE = kv ? (int)B_VE : (int)B_KE;
             const auto* draft_rows = static_cast<const __nv_bfloat16*>(kv ? a.v_draft : a.k_draft);
             bool ok = true;
@@ -330,9 +341,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 const int bg = tile / g.tiles_bg, b = bg / g.Hkv;
                 int len, nodes;
                 tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes);
+                ListWindow win;
+                win.start(w.list + (size_t)tile * g.lcap, e0, e0 + n);
                 for (int s = 0; s < n; ++s) {
                     const int gs = gs0 + s, st = gs % NS, rst = rs % kTtRaw;
-                    const int j = w.list[(size_t)tile * g.lcap + e0 + s];
+                    win.to(e0 + s);
+                    const int j = win.at(e0 + s);
                     const bool draft = j == kTreeDraft;
                     const int lim = draft ? nodes : j == kTreeOpen ? len % kBlock : kBlock;   // rows that are there
                     if (!draft) {
@@ -343,7 +357,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     if (!ok) continue;
                     const uint8_t* rp = base_ptr + L::off_raw + rst * L::kRaw;
                     uint8_t* dst = base_ptr + (kv ? L::off_v : L::off_k) + st * L::kTile;
-                    constexpr int IT = kBlock * CH / 64;
+                    constexpr int IT = kBlock * CH / CT;
                     // chunks 2 c and 2 c + 1 of a row's half; the upper half's lanes store the odd chunk
                     // first, so the lanes of a phase fall in distinct banks
                     const int c = ct % CH, sw = c >> 2, c0 = (c & 3) * 2;
@@ -361,7 +375,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     };
                     const uint8_t* codes = rp + kv * L::kRawKV + ct * 16;
                     const uint8_t* scales = rp + 2 * L::kRawKV + kv * 64 + ct / CH;
-                    constexpr int RS = 64 / CH;                  // rows per round of the 64 threads
+                    constexpr int RS = CT / CH;                  // rows per round of the threads
                     if (j >= 0) {
                         constexpr int U4 = IT < 4 ? IT : 4;
 #pragma unroll 1
@@ -370,7 +384,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                             uint32_t sb[U4];
 #pragma unroll
                             for (int i = 0; i < U4; ++i) {
-                                x[i] = *reinterpret_cast<const uint4*>(codes + (it0 + i) * 1024);
+                                x[i] = *reinterpret_cast<const uint4*>(codes + (it0 + i) * CT * 16);
                                 sb[i] = scales[(it0 + i) * RS];
                             }
 #pragma unroll
@@ -392,7 +406,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                                     lo = __ldg(p);
                                     hi = __ldg(p + 1);
                                 } else {
-                                    convert(*reinterpret_cast<const uint4*>(codes + it * 1024), scales[it * RS], &lo, &hi);
+                                    convert(*reinterpret_cast<const uint4*>(codes + it * CT * 16), scales[it * RS], &lo, &hi);
                                 }
                             }
                             store(r, lo, hi);
@@ -406,10 +420,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
     } else {
         // ------------------------------------------------------------ softmax groups
+        if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;" ::: "memory");
         const int grp = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t s_col = grp * 64, o_col = L::colO + grp * D, l_col = L::colL + grp * 16;
-        uint8_t* const prow0 = base_ptr + L::off_p + kTtPBuf * grp * L::kP + (r >> 3) * 1024 + (r & 7) * 128;
+        const uint32_t s_col = grp * 64, o_col = L::colO + grp * D, p_col = L::colP + grp * 32;
         bool ok = true;
         auto wwait = [&](uint32_t bar_addr, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, abort_flag));
@@ -418,40 +432,53 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const int bg = tile / g.tiles_bg, b = bg / g.Hkv, row_g = (tile % g.tiles_bg) * kTreeRows + r;
             const bool in_tile = row_g < g.R;
             const size_t row = (size_t)bg * g.R + row_g;
-            // Q tile: two threads per row
-            {
-                const int half = grp;                            // this group's dims of the row
-                const uint4* src = reinterpret_cast<const uint4*>(q + row * D) + half * (D / 16);
-#pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    const uint4 v = in_tile ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-                    const int cc = half * (D / 16) + c;
-                    *reinterpret_cast<uint4*>(base_ptr + L::off_q + (cc >> 3) * L::kQHalf + r * 128 + (((cc & 7) ^ (r & 7)) << 4)) = v;
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(bar(B_Q));
-            }
+            // everything that depends on the tile alone is on its way before any of it is used
             int len, nodes;
             tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes);
-            const int F = len / kBlock, rem = len % kBlock, node = in_tile ? row_g % g.N : 0;
-            const size_t bn = (size_t)b * g.N;
-            const unsigned long long anc = in_tile && node < nodes ? w.anc[bn + node] : 0ull;
-            const bool valid = anc != 0ull;
-            const bool warp_live = __any_sync(0xffffffffu, valid);
-            const float tau_r = valid ? w.tau[row] : __int_as_float(0x7fc00000);
-            const float* xr = w.xs + row * g.cap;
-            const bool crossed = valid && rem + w.depth[bn + node] >= kBlock;
-            const float xF = crossed ? xr[F] : 0.f;
-            // log2 prior of the open block's keys: 1 while it is the own block
-            const float lpo = !crossed ? 0.f : (xF > tau_r ? e_pow * __log2f(xF - tau_r) : -INFINITY);
-            auto entry = [&](int s) { return s < n ? w.list[(size_t)tile * g.lcap + e0 + s] : kTreeDraft; };
-            auto xval = [&](int j) { return valid && j >= 0 ? __ldcg(xr + j) : 0.f; };
+            auto entry = [&](int s) { return s < n ? __ldcg(w.list + (size_t)tile * g.lcap + e0 + s) : kTreeDraft; };
             const int s0 = (gs0 & 1) == grp ? 0 : 1;
             int j0 = entry(s0), j1 = entry(s0 + 2);
+            const int node = in_tile ? row_g % g.N : 0;
+            const size_t bn = (size_t)b * g.N;
+            unsigned long long anc = in_tile ? __ldcg(w.anc + bn + node) : 0ull;
+            const int dep = in_tile ? __ldcg(w.depth + bn + node) : 0;
+            const float tau_m = in_tile ? __ldcg(w.tau + row) : 0.f;
+            // group 0 brings the tile's rows of Q into TMEM, row r in lane r (zeros for rows it lacks)
+            if (grp == 0) {
+                const uint4* src = reinterpret_cast<const uint4*>(q + row * D);
+                auto load = [&](int c) { return in_tile ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u); };
+#pragma unroll
+                for (int f = 0; f < D / 32; ++f) {
+                    uint4 v[4];
+                    uint32_t w16[16];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[c] = load(f * 4 + c);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        w16[4 * c] = v[c].x; w16[4 * c + 1] = v[c].y;
+                        w16[4 * c + 2] = v[c].z; w16[4 * c + 3] = v[c].w;
+                    }
+                    tmem_st16(lane_addr + L::colQ + f * 16, w16);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(B_Q));
+            }
+            const int F = len / kBlock, rem = len % kBlock;
+            if (node >= nodes) anc = 0ull;
+            const bool valid = anc != 0ull;
+            const bool warp_live = __any_sync(0xffffffffu, valid);
+            const float tau_r = valid ? tau_m : __int_as_float(0x7fc00000);
+            const float* xr = w.xs + row * g.cap;
+            const bool crossed = valid && rem + dep >= kBlock;
+            auto xval = [&](int j) { return valid && j >= 0 ? __ldcg(xr + j) : 0.f; };
+            const float xF = crossed ? __ldcg(xr + F) : 0.f;
             float x0 = xval(j0);
-            float m_run = -INFINITY;
+            // log2 prior of the open block's keys: 1 while it is the own block
+            const float lpo = !crossed ? 0.f : (xF > tau_r ? e_pow * __log2f(xF - tau_r) : -INFINITY);
+            float m_run = -INFINITY, l_run = 0.f;
             for (int s = s0; s < n; s += 2) {
-                const int gs = gs0 + s, i2 = gs >> 1, pb = i2 % kTtPBuf;
+                const int gs = gs0 + s, i2 = gs >> 1;
                 const float x1 = xval(j1);                       // the next steps' values, on their way early
                 const int j2 = entry(s + 4);
                 const int j = j0;
@@ -459,52 +486,67 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 j0 = j1; j1 = j2; x0 = x1;
                 if (!(ok && wwait(bar(B_SF + grp), i2 & 1))) { ok = false; continue; }
                 if (!warp_live) {
-                    // no row of this warp is used; its lanes of S, P and O hold whatever they hold
+                    // no row of this warp is used; its lanes of S, P and O hold whatever they hold.  It
+                    // still waits for the product before, so as not to count towards an earlier P
                     mbar_arrive(bar(B_SE + grp));
-                    mbar_arrive(bar(B_PF + kTtPBuf * grp + pb));
+                    if (i2 >= 1 && !wwait(bar(B_PD + grp), (i2 - 1) & 1)) { ok = false; continue; }
+                    mbar_arrive(bar(B_PF + grp));
                     continue;
                 }
+                float scale = sm2;
                 tc_fence_after();
-                uint32_t sr[64];
-                tmem_ld<64>(lane_addr + s_col, sr);
-                tmem_wait_ld();
-                tc_fence_before();
-                mbar_arrive(bar(B_SE + grp));
-                float scale = sm2, lp2;
+                float lp2;
+                unsigned long long on = 0ull, low = 0ull;        // special entries: attended keys, those with prior lpo
                 if (j >= 0) {
                     lp2 = valid && x > tau_r ? e_pow * __log2f(x - tau_r) : -INFINITY;
-                } else if (j == kTreeOpen) {
-                    lp2 = valid ? lpo : -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (i >= rem) sr[i] = __float_as_uint(-INFINITY);
                 } else {
-                    // the draft: ancestors and self; those in a completed open block carry its prior
-                    unsigned long long low = 0ull;
-                    if (crossed)
-                        for (int i = 0; i < nodes; ++i)
-                            if (rem + w.depth[bn + i] < kBlock) low |= 1ull << i;
-                    lp2 = valid ? 0.f : -INFINITY;
-                    scale = 1.f;
-                    const uint32_t a0 = (uint32_t)anc, a1 = (uint32_t)(anc >> 32), l0 = (uint32_t)low, l1 = (uint32_t)(low >> 32);
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        const uint32_t am = i < 32 ? a0 : a1, lm = i < 32 ? l0 : l1;
-                        float v = __uint_as_float(sr[i]) * sm2;
-                        if ((lm >> (i & 31)) & 1u) v = lpo == -INFINITY ? -INFINITY : v + lpo;
-                        if (!((am >> (i & 31)) & 1u)) v = -INFINITY;
-                        sr[i] = __float_as_uint(v);
+                    // the open block's keys (those before the sequence's end), or the draft's (ancestors
+                    // and self; those in a completed open block carry its prior)
+                    if (j == kTreeOpen) {
+                        on = low = (1ull << rem) - 1ull;
+                    } else {
+                        on = anc;
+                        if (crossed)
+                            for (int i = 0; i < nodes; ++i)
+                                if (rem + w.depth[bn + i] < kBlock) low |= 1ull << i;
                     }
+                    lp2 = valid ? 0.f : -INFINITY;
                 }
+                uint32_t sr[64];
                 float mx = -INFINITY;
-                if (lp2 > -INFINITY) {
+                // rows that do not attend this entry skip its scores: whole warps of them often do
+                if (__any_sync(0xffffffffu, lp2 > -INFINITY)) {
+                    if (j < 0) {
+                        // finished logits in place of the scores, -inf where a key is not attended; back
+                        // to TMEM 16 at a time, in a loop: rare code that is kept small
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 16) {
+                            uint32_t t[16];
+                            tmem_ld16(lane_addr + s_col + c, t);
+                            tmem_wait_ld();
+                            const uint32_t om = (uint32_t)(on >> c), lm = (uint32_t)(low >> c);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float v = __uint_as_float(t[i]) * sm2;
+                                if ((lm >> i) & 1u) v = lpo == -INFINITY ? -INFINITY : v + lpo;
+                                t[i] = __float_as_uint((om >> i) & 1u ? v : -INFINITY);
+                            }
+                            tmem_st16(lane_addr + s_col + c, t);
+                        }
+                        tmem_wait_st();
+                        scale = 1.f;
+                    }
+                    tmem_ld<64>(lane_addr + s_col, sr);
+                    tmem_wait_ld();
                     float m4[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) m4[i] = fmaxf(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]));
 #pragma unroll
                     for (int i = 4; i < 32; ++i) m4[i & 3] = max3(m4[i & 3], __uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]));
-                    mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), scale, lp2);
+                    if (lp2 > -INFINITY) mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), scale, lp2);
                 }
+                tc_fence_before();
+                mbar_arrive(bar(B_SE + grp));
                 const bool active = mx > -INFINITY;
                 float factor = 1.f;
                 bool resc = false;
@@ -512,96 +554,93 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     if (m_run == -INFINITY) m_run = mx;
                     else if (mx > m_run + kTtLazy) { factor = exp2f(m_run - mx); m_run = mx; resc = true; }
                 }
-                uint8_t* const prow = prow0 + pb * L::kP;
                 const float c0 = lp2 - m_run;
                 const uint64_t sc2 = f2_pack(__float_as_uint(scale), __float_as_uint(scale));
                 const uint64_t c2 = f2_pack(__float_as_uint(c0), __float_as_uint(c0));
+                uint32_t pk[32];
+                uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t pk[4] = {0u, 0u, 0u, 0u};
+                for (int i = 0; i < 32; ++i) {
+                    pk[i] = 0u;
                     if (active) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float v0, v1;
-                            f2_unpack(f2_fma(f2_pack(sr[c * 8 + 2 * i], sr[c * 8 + 2 * i + 1]), sc2, c2), v0, v1);
-                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(fast_exp2(v0), fast_exp2(v1));
-                            pk[i] = *reinterpret_cast<const uint32_t*>(&h2);
-                        }
+                        float v0, v1;
+                        f2_unpack(f2_fma(f2_pack(sr[2 * i], sr[2 * i + 1]), sc2, c2), v0, v1);
+                        v0 = fast_exp2(v0);
+                        v1 = fast_exp2(v1);
+                        sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(__float_as_uint(v0), __float_as_uint(v1)));
+                        const __nv_bfloat162 h2 = __floats2bfloat162_rn(v0, v1);
+                        pk[i] = *reinterpret_cast<const uint32_t*>(&h2);
                     }
-                    *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                 }
-                if (__any_sync(0xffffffffu, resc)) {
-                    // the group's previous product has landed before O and the row sums are rescaled
-                    if (!wwait(bar(B_PD + kTtPBuf * grp + (i2 - 1) % kTtPBuf), ((i2 - 1) / kTtPBuf) & 1)) { ok = false; continue; }
+                {
+                    float a0, a1;
+                    f2_unpack(f2_add(sum2[0], sum2[1]), a0, a1);
+                    l_run = fmaf(l_run, factor, a0 + a1);
+                }
+                // the group's previous product has read P and written O
+                if (i2 >= 1) {
+                    if (!wwait(bar(B_PD + grp), (i2 - 1) & 1)) { ok = false; continue; }
                     tc_fence_after();
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(lane_addr + o_col + c * 32, o);
+                }
+                tmem_st32(lane_addr + p_col, pk);
+                if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll 2
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t o[16];
+                        tmem_ld16(lane_addr + o_col + c * 16, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-                        tmem_st32(lane_addr + o_col + c * 32, o);
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+                        tmem_st16(lane_addr + o_col + c * 16, o);
                     }
-                    uint32_t o[16];
-                    tmem_ld16(lane_addr + l_col, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-                    tmem_st16(lane_addr + l_col, o);
-                    tmem_wait_st();
                 }
-                fence_proxy_async_smem();
+                tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar(B_PF + kTtPBuf * grp + pb));
+                mbar_arrive(bar(B_PF + grp));
             }
             if (tid == 0 && e0 == 0) w.offs[tile] = o0;          // for the merge of a split tile
             // ---- the two groups' states: (max, sum, output) of every row
             m_sh[grp][r] = m_run;
+            l_sh[grp][r] = l_run;
             asm volatile("bar.sync 1, 256;" ::: "memory");
             const int gl = gs0 + n - 1;                          // last step; the other group's last is before it
             const bool both = n >= 2;
             bool done = ok;
-            {
-                const int i2 = gl >> 1, p = kTtPBuf * (gl & 1) + i2 % kTtPBuf;
-                done = done && wwait(bar(B_PD + p), (i2 / kTtPBuf) & 1);
-            }
-            if (both) {
-                const int i2 = (gl - 1) >> 1, p = kTtPBuf * ((gl - 1) & 1) + i2 % kTtPBuf;
-                done = done && wwait(bar(B_PD + p), (i2 / kTtPBuf) & 1);
-            }
+            done = done && wwait(bar(B_PD + (gl & 1)), (gl >> 1) & 1);
+            if (both) done = done && wwait(bar(B_PD + ((gl - 1) & 1)), ((gl - 1) >> 1) & 1);
             if (done && warp_live) {
                 tc_fence_after();
                 const bool has0 = both || (gl & 1) == 0, has1 = both || (gl & 1) == 1;
                 const float m0 = has0 ? m_sh[0][r] : -INFINITY, m1 = has1 ? m_sh[1][r] : -INFINITY;
                 const float M = fmaxf(m0, m1);
                 const float w0 = m0 == -INFINITY ? 0.f : exp2f(m0 - M), w1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
-                const float l0 = __uint_as_float(tmem_ld1(lane_addr + L::colL)), l1 = __uint_as_float(tmem_ld1(lane_addr + L::colL + 16));
-                tmem_wait_ld();
+                const float l0 = l_sh[0][r], l1 = l_sh[1][r];
                 const float den = (w0 > 0.f ? l0 * w0 : 0.f) + (w1 > 0.f ? l1 * w1 : 0.f);
                 const bool direct = dt_cta_of(o0, U, nC) == dt_cta_of(o1 - 1, U, nC);
-                float* pr = w.part + (((size_t)cta + tile) * kTreeRows + r) * (D + 4);
-                if (!direct && valid && grp == 0) { pr[0] = M; pr[1] = den; }
+                // partial of a tile: (max, sum) per row, then the outputs as [dims / 4][row][4], which
+                // the lanes of a warp (rows) write side by side
+                float* pr = w.part + ((size_t)cta + tile) * kTreeRows * (D + 4);
+                if (!direct && valid && grp == 0) *reinterpret_cast<float2*>(pr + 2 * r) = make_float2(M, den);
                 const float inv = direct ? 1.0f / den : 1.0f;
                 auto* out = static_cast<__nv_bfloat16*>(a.out) + row * D;
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    const int col = grp * (D / 2) + c * 32;      // the groups share the row's columns
-                    uint32_t p0[32], p1[32];
-                    tmem_ld32(lane_addr + L::colO + col, p0);
-                    tmem_ld32(lane_addr + L::colO + D + col, p1);
+#pragma unroll 2
+                for (int c = 0; c < D / 32; ++c) {
+                    const int col = grp * (D / 2) + c * 16;      // the groups share the row's columns
+                    uint32_t p0[16], p1[16];
+                    tmem_ld16(lane_addr + L::colO + col, p0);
+                    tmem_ld16(lane_addr + L::colO + D + col, p1);
                     tmem_wait_ld();
                     if (valid) {
-                        float f[32];
+                        float f[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
+                        for (int i = 0; i < 16; ++i) {
                             float v = w0 > 0.f ? __uint_as_float(p0[i]) * w0 : 0.f;
                             if (w1 > 0.f) v = fmaf(__uint_as_float(p1[i]), w1, v);
                             f[i] = v * inv;
                         }
                         if (direct) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                            for (int i = 0; i < 2; ++i) {
                                 uint32_t pk[4];
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
@@ -612,7 +651,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                             }
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(pr + 4 + col + 4 * i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<float4*>(pr + 4 * kTreeRows + ((col / 4 + i) * kTreeRows + r) * 4) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
                         }
                     }
                 }
@@ -631,14 +671,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     if (tid == 0 && abort_sh) atomicOr(&w.hdr->status, kStWaitTimeout);
 }
 
-// One warp per row of a tile that several CTAs share: merges their partials.
+// Merges the partials of a tile that several CTAs share: a CTA takes 1024 / D rows, a warp their
+// weights (lanes over the pieces), then a thread four dims of a row, the lanes side by side in
+// the partials' [dims / 4][row] order and eight pieces in flight.
 template <int D>
 __global__ void __launch_bounds__(256)
 tree_combine_kernel(TreeArgs a, TreeWork w, TreeGeom g, int nctas, int per) {
-    constexpr int kPerTile = kTreeRows / 8, DPL = D / 32;
-    const int tile = blockIdx.x / kPerTile, r = (blockIdx.x % kPerTile) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int bg = tile / g.tiles_bg, b = bg / g.Hkv, row_g = (tile % g.tiles_bg) * kTreeRows + r;
-    if (row_g >= g.R) return;
+    constexpr int RPC = 1024 / D, kPerTile = kTreeRows / RPC;
+    __shared__ float wt_sh[RPC][kDecodeMaxCtas], inv_sh[RPC];
+    const int tile = blockIdx.x / kPerTile, r0 = (blockIdx.x % kPerTile) * RPC;
+    const int bg = tile / g.tiles_bg, b = bg / g.Hkv, row0 = (tile % g.tiles_bg) * kTreeRows + r0;
+    if (row0 >= g.R) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     const int n = w.count[tile];
     if (n == 0) return;
@@ -649,54 +693,51 @@ tree_combine_kernel(TreeArgs a, TreeWork w, TreeGeom g, int nctas, int per) {
     if (c0 == c1) return;
     int len, nodes;
     if (!tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes)) return;
-    const int node = row_g % g.N;
-    if (node >= nodes || !w.anc[(size_t)b * g.N + node]) return;
-    const float* p = w.part + (((size_t)c0 + tile) * kTreeRows + r) * (D + 4);
+    const float* p = w.part + ((size_t)c0 + tile) * kTreeRows * (D + 4);
     const size_t step = (size_t)kTreeRows * (D + 4);
     const int np = c1 - c0 + 1;
-    float M = -INFINITY, den = 0.f;
-    for (int i = lane; i < np; i += 32) M = fmaxf(M, __ldcg(p + i * step));
-    M = warp_max(M);
-    float num[DPL];
-#pragma unroll
-    for (int d = 0; d < DPL; ++d) num[d] = 0.f;
-    for (int i0 = 0; i0 < np; i0 += 32) {
-        // lane i holds piece i's weight
-        float wt = 0.f;
-        if (i0 + lane < np) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + (i0 + lane) * step));
-            wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+    for (int rr = warp; rr < RPC; rr += 8) {
+        const int row_g = row0 + rr, node = row_g % g.N;
+        if (row_g >= g.R || node >= nodes || !w.anc[(size_t)b * g.N + node]) {
+            if (lane == 0) inv_sh[rr] = -1.f;                    // no such row, or none to merge
+            continue;
+        }
+        const float* ph = p + 2 * (r0 + rr);
+        float M = -INFINITY, den = 0.f;
+        for (int i = lane; i < np; i += 32) M = fmaxf(M, __ldcg(ph + i * step));
+        M = warp_max(M);
+        for (int i = lane; i < np; i += 32) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(ph + i * step));
+            const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+            wt_sh[rr][i] = wt;
             den = fmaf(ml.y, wt, den);
         }
-        const int kn = min(32, np - i0);
-        constexpr int KB = 8;                          // pieces whose loads are in flight together
-        for (int k0 = 0; k0 < kn; k0 += KB) {
-            float v[KB][DPL];
+        den = warp_sum(den);
+        if (lane == 0) inv_sh[rr] = 1.0f / den;
+    }
+    __syncthreads();
+    const int rr = tid % RPC, c4 = tid / RPC;
+    const float inv = inv_sh[rr];
+    if (inv < 0.f) return;
+    const float* po = p + 4 * kTreeRows + ((size_t)c4 * kTreeRows + r0 + rr) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int KB = 8;
+    for (int i0 = 0; i0 < np; i0 += KB) {
+        float4 v[KB];
 #pragma unroll
-            for (int k = 0; k < KB; ++k) {
-                // past the last piece: that piece again, with weight 0
-                const float* pi = p + (i0 + min(k0 + k, kn - 1)) * step + 4 + lane * DPL;
-                if constexpr (DPL == 4) {
-                    const float4 t = __ldcg(reinterpret_cast<const float4*>(pi));
-                    v[k][0] = t.x; v[k][1] = t.y; v[k][2] = t.z; v[k][3] = t.w;
-                } else {
-                    const float2 t = __ldcg(reinterpret_cast<const float2*>(pi));
-                    v[k][0] = t.x; v[k][1] = t.y;
-                }
-            }
+        for (int k = 0; k < KB; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(po + min(i0 + k, np - 1) * step));
 #pragma unroll
-            for (int k = 0; k < KB; ++k) {
-                const float wk = k0 + k < kn ? __shfl_sync(0xffffffffu, wt, k0 + k) : 0.f;
-#pragma unroll
-                for (int d = 0; d < DPL; ++d) num[d] = fmaf(v[k][d], wk, num[d]);
-            }
+        for (int k = 0; k < KB; ++k) {
+            const float wt = i0 + k < np ? wt_sh[rr][i0 + k] : 0.f;
+            acc.x = fmaf(v[k].x, wt, acc.x);
+            acc.y = fmaf(v[k].y, wt, acc.y);
+            acc.z = fmaf(v[k].z, wt, acc.z);
+            acc.w = fmaf(v[k].w, wt, acc.w);
         }
     }
-    den = warp_sum(den);
-    const float inv = 1.0f / den;
-    auto* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)bg * g.R + row_g) * D + lane * DPL;
-#pragma unroll
-    for (int d = 0; d < DPL / 2; ++d) *reinterpret_cast<__nv_bfloat162*>(out + 2 * d) = __floats2bfloat162_rn(num[2 * d] * inv, num[2 * d + 1] * inv);
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + ((size_t)bg * g.R + row0 + rr) * D + c4 * 4) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 template <int D, bool Q8>
@@ -712,10 +753,10 @@ static cudaError_t launch_t(const TreeArgs& a, const TreeWork& w, const TreeGeom
     const int sm = (int)TtLayout<D, Q8>::bytes;
     cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
     if (e != cudaSuccess) return e;
-    const PdlConfig ca(nctas, Q8 ? 512 : 384, sm, stream);
+    const PdlConfig ca(nctas, kTtThreads<Q8>, sm, stream);
     e = cudaLaunchKernelEx(&ca.cfg, tree_attn_kernel<D, Q8>, tk, tv, tkd, tvd, a, w, g, e_pow, sm2, per);
     if (e != cudaSuccess) return e;
-    const PdlConfig cc((unsigned)g.tiles * (kTreeRows / 8), 256, 0, stream);
+    const PdlConfig cc((unsigned)g.tiles * (kTreeRows * D / 1024), 256, 0, stream);
     e = cudaLaunchKernelEx(&cc.cfg, tree_combine_kernel<D>, a, w, g, nctas, per);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
