@@ -20,9 +20,9 @@
 //
 // 8-bit cache: warp 8 streams codes and scale bytes with bulk copies into a ring of their own, and
 // warps 12 - 15 (K) and 16 - 19 (V) turn them into bf16 operand tiles (exact: cache8.cuh) or load
-// the draft's bf16 rows.  Two warps a tensor convert too slowly (32K, 8 x 16 nodes: 112 us a step
-// against 98); tiles of f16 codes with the scales outside the product save conversions but need
-// another factor per step in every role, and measured 115.
+// the draft's bf16 rows.  Two warps a tensor convert too slowly (32K, 8 x 24 rows: 112 us a step
+// against 93), eight gain nothing; tiles of f16 codes with the scales outside the product save
+// conversions but need another factor per step in every role, and measured 115.
 // Every wait is bounded; a CTA that gives up sets a status bit.
 #include "cache8.cuh"
 #include "kernels.h"
@@ -98,18 +98,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const auto* q = static_cast<const __nv_bfloat16*>(a.q);
     if (tid == 0) {
         abort_sh = 0;
-        const int conv = Q8 ? kTtConv * 32 : 1;                          // who fills an operand tile
-        mbar_init(bar(B_Q), 128);
+        const int conv = Q8 ? kTtConv : 1;                      // who fills an operand tile
+        mbar_init(bar(B_Q), 4);
         for (int i = 0; i < KS; ++i) { mbar_init(bar(B_KF + i), conv); mbar_init(bar(B_KE + i), 1); }
         for (int i = 0; i < VS; ++i) { mbar_init(bar(B_VF + i), conv); mbar_init(bar(B_VE + i), 1); }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(B_SF + i), 1);
-            mbar_init(bar(B_SE + i), 128);
-            mbar_init(bar(B_PF + i), 128);
+            mbar_init(bar(B_SE + i), 4);
+            mbar_init(bar(B_PF + i), 4);
             mbar_init(bar(B_PD + i), 1);
             mbar_init(bar(B_DR + i), 1);
         }
-        for (int i = 0; i < kTtRaw; ++i) { mbar_init(bar(B_RF + i), 1); mbar_init(bar(B_RE + i), kTtConv * 64); }
+        for (int i = 0; i < kTtRaw; ++i) { mbar_init(bar(B_RF + i), 1); mbar_init(bar(B_RE + i), 2 * kTtConv); }
         mbar_init(bar(B_VT), 1);
         fence_mbar_init();
     }
@@ -134,6 +134,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     volatile int* abort_flag = &abort_sh;
     auto k_addr = [&](int st) { return base + L::off_k + (uint32_t)st * L::kTile; };
     auto v_addr = [&](int st) { return base + L::off_v + (uint32_t)st * L::kTile; };
+
+    // one arrival a warp: 32 lanes' arrivals at one barrier are served one after another
+    auto arrive = [&](uint32_t bar_addr) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_addr);
+    };
 
     // calls body(tile, first entry, entries, steps before, the tile's first entry in the
     // concatenation, its end) for every segment of the range
@@ -336,24 +342,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const int bF = kv ? (int)B_VF : (int)B_KF, bE = kv ? (int)B_VE : (int)B_KE;
             const auto* draft_rows = static_cast<const __nv_bfloat16*>(kv ? a.v_draft : a.k_draft);
             bool ok = true;
-            int rs = 0;                                          // raw stages taken
-            segments([&](int tile, int e0, int n, int gs0, int, int) {
+            int rst = 0, st = 0;                                 // stages of the rings, and the parities of their
+            uint32_t rph = 0, ph = 1;                            // waits (a fresh ring's tiles are free)
+            segments([&](int tile, int e0, int n, int, int, int) {
                 const int bg = tile / g.tiles_bg, b = bg / g.Hkv;
                 int len, nodes;
                 tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes);
                 ListWindow win;
                 win.start(w.list + (size_t)tile * g.lcap, e0, e0 + n);
                 for (int s = 0; s < n; ++s) {
-                    const int gs = gs0 + s, st = gs % NS, rst = rs % kTtRaw;
                     win.to(e0 + s);
                     const int j = win.at(e0 + s);
                     const bool draft = j == kTreeDraft;
                     const int lim = draft ? nodes : j == kTreeOpen ? len % kBlock : kBlock;   // rows that are there
                     if (!draft) {
-                        ok = ok && mbar_wait(bar(B_RF + rst), (rs / kTtRaw) & 1, abort_flag);
-                        ++rs;
+                        ok = ok && mbar_wait(bar(B_RF + rst), rph, abort_flag);
                     }
-                    ok = ok && (gs < NS || mbar_wait(bar(bE + st), ((gs / NS) - 1) & 1, abort_flag));
+                    ok = ok && mbar_wait(bar(bE + st), ph, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) continue;
                     const uint8_t* rp = base_ptr + L::off_raw + rst * L::kRaw;
                     uint8_t* dst = base_ptr + (kv ? L::off_v : L::off_k) + st * L::kTile;
@@ -413,8 +419,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         }
                     }
                     fence_proxy_async_smem();
-                    mbar_arrive(bar(bF + st));
-                    if (!draft) mbar_arrive(bar(B_RE + rst));
+                    arrive(bar(bF + st));
+                    if (!draft) {
+                        arrive(bar(B_RE + rst));
+                        if (++rst == kTtRaw) { rst = 0; rph ^= 1u; }
+                    }
+                    if (++st == NS) { st = 0; ph ^= 1u; }
                 }
             });
         }
@@ -462,7 +472,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar(B_Q));
+                arrive(bar(B_Q));
             }
             const int F = len / kBlock, rem = len % kBlock;
             if (node >= nodes) anc = 0ull;
@@ -488,9 +498,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 if (!warp_live) {
                     // no row of this warp is used; its lanes of S, P and O hold whatever they hold.  It
                     // still waits for the product before, so as not to count towards an earlier P
-                    mbar_arrive(bar(B_SE + grp));
+                    arrive(bar(B_SE + grp));
                     if (i2 >= 1 && !wwait(bar(B_PD + grp), (i2 - 1) & 1)) { ok = false; continue; }
-                    mbar_arrive(bar(B_PF + grp));
+                    arrive(bar(B_PF + grp));
                     continue;
                 }
                 float scale = sm2;
@@ -546,7 +556,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     if (lp2 > -INFINITY) mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), scale, lp2);
                 }
                 tc_fence_before();
-                mbar_arrive(bar(B_SE + grp));
+                arrive(bar(B_SE + grp));
                 const bool active = mx > -INFINITY;
                 float factor = 1.f;
                 bool resc = false;
@@ -596,7 +606,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar(B_PF + grp));
+                arrive(bar(B_PF + grp));
             }
             if (tid == 0 && e0 == 0) w.offs[tile] = o0;          // for the merge of a split tile
             // ---- the two groups' states: (max, sum, output) of every row
