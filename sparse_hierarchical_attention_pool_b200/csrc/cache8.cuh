@@ -22,8 +22,8 @@
 
 namespace dash {
 
-constexpr int kScaleMin = -118, kScaleMax = 120;
-constexpr float kHeldMax = 240.0f * 0x1p120f;   // largest held magnitude: 256 2^120 would be no bf16 number
+constexpr int kScaleMin = -118;
+constexpr unsigned kHeldTop = 0x7f70u;          // bf16 bits of the largest held magnitude, 240 2^120 (256 2^120 would be no bf16 number)
 constexpr unsigned kScaleNaN = 255u;
 
 // 2^(s - 127) for the scale bytes the cache holds (9 .. 247), NaN for kScaleNaN

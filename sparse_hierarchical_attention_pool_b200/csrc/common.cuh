@@ -222,11 +222,11 @@ struct TreeGeom {
     int B, Hq, Hkv, N, Tmax, d, G, nbs;
     int R;                           // rows per KV group = G * N
     int tiles_bg, tiles;             // tiles per KV group, in all
-    int cap;                         // scores per row: the full blocks and the open one
+    int cap;                         // scores per row: the full blocks and the open one, and padding
     int lcap;                        // list entries per tile: the full blocks, the open one, the tree
     int nbw;                         // 32-bit words of a tile's selection bitmap
     int maxit;
-    size_t off_x, off_tau, off_anc, off_depth, off_path, off_bits, off_tick, off_list, off_count, off_offs, off_part,
+    size_t off_x, off_tau, off_anc, off_depth, off_path, off_bits, off_tick, off_list, off_count, off_part,
         total;
 };
 
@@ -239,9 +239,9 @@ inline bool make_tree_geom(int B, int Hq, int Hkv, int N, int Tmax, int d, TreeG
     g->R = g->G * N;
     g->tiles_bg = (g->R + kTreeRows - 1) / kTreeRows;
     g->tiles = B * Hkv * g->tiles_bg;
-    g->cap = g->nbs + 1;
+    g->cap = (g->nbs + 4) & ~3;      // rows of scores begin on 16 bytes
     g->lcap = g->nbs + 2;
-    g->nbw = (g->cap + 31) / 32;
+    g->nbw = (g->nbs + 32) / 32;
     g->maxit = solve_cap_from_env();
     const size_t rows = (size_t)B * Hq * N, tiles = (size_t)g->tiles;
     size_t off = align256(sizeof(WsHeader));
@@ -254,7 +254,6 @@ inline bool make_tree_geom(int B, int Hq, int Hkv, int N, int Tmax, int d, TreeG
     g->off_tick = off;  off = align256(off + tiles * sizeof(int));
     g->off_list = off;  off = align256(off + tiles * g->lcap * sizeof(int));
     g->off_count = off; off = align256(off + tiles * sizeof(int));
-    g->off_offs = off;  off = align256(off + (tiles + 1) * sizeof(int));
     // partial (max, sum, padding to 16 bytes, output) per row of a (CTA + tile) slot
     g->off_part = off;  off = align256(off + (tiles + kDecodeMaxCtas) * kTreeRows * (d + 4) * sizeof(float));
     g->total = off;

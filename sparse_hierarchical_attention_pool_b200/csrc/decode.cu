@@ -252,7 +252,7 @@ decode_select_kernel(const int* __restrict__ kv_len, const float* __restrict__ x
                      float* __restrict__ tau, int* __restrict__ list, int* __restrict__ count,
                      int* __restrict__ done, int* __restrict__ offs, int* __restrict__ plan,
                      __nv_bfloat16* __restrict__ out, WsHeader* __restrict__ hdr, DecodeGeom g,
-                     float alpha, int nctas, int hist_init) {
+                     float alpha, int nctas, int hist_init, bool warm) {
     constexpr int kWords = kMaxT / kBlock / 32;
     __shared__ HistBins hist[kSelThreads / 32];
     __shared__ unsigned bitmap[kWords];
@@ -284,7 +284,8 @@ decode_select_kernel(const int* __restrict__ kv_len, const float* __restrict__ x
         WarpRow xr;
         xr.load(xs + row * cap, rows_sm + (size_t)warp * scap, scap, lane, bt);
         float t = __int_as_float(0x7fc00000);
-        if (bt > 0) t = row_tau(xr, xr.max(), alpha, &no_conv, hist_init ? &hist[warp] : nullptr, g.maxit);
+        const float y = xr.lane_max(), m = warp_max(y);
+        if (bt > 0) t = row_tau(xr, m, alpha, &no_conv, hist_init ? &hist[warp] : nullptr, g.maxit, warm ? lane_start(y - m, alpha) : -1.0f);
         if (lane == 0) tau[row] = t;
         const int nsel = xr.words(t, [&](int k, unsigned w) { atomicOr(&bitmap[k], w); });
         if (lane == 0) {
@@ -494,7 +495,7 @@ cudaError_t launch_decode_lists(const void* q, const float* ksum, const int* kv_
                            reinterpret_cast<int*>(ws + gl.off_list), reinterpret_cast<int*>(ws + gl.off_count),
                            reinterpret_cast<int*>(ws + gl.off_done), reinterpret_cast<int*>(ws + gl.off_offs),
                            reinterpret_cast<int*>(ws + gl.off_plan), static_cast<__nv_bfloat16*>(out), hdr, gl, alpha, nctas,
-                           hist_init);
+                           hist_init, pdl);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

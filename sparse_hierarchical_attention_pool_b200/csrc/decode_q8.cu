@@ -47,7 +47,8 @@ constexpr int kQ8Keys = 32;          // keys per unit: a consumer's share of an 
 // the same two consumers: each waits for a stage only after it has used the entry before, and
 // the wait never meets a barrier that is still a phase behind.
 static_assert(kQ8Warps == 4 && kQ8Stages % 2 == 0, "a stage keeps its consumers");
-constexpr int kQ8Per = 4;            // list entries per CTA at least
+constexpr int kQ8Per = 6;            // list entries per CTA at least (16K, 2 KV heads: 4 entries 22.6 us a step, 6 21.2, 8 21.0;
+                                     // 5K of 64 dims: 19.7, 20.2, 20.8)
 constexpr int kQ8PartHead = 4;       // floats of a partial before its output: mA, sum, mB, -
 constexpr float kWBits = 12.0f;      // weights reach 2^12: f16 then keeps terms down to 2^-36 of the largest
 
@@ -93,8 +94,8 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 2)
 decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vs,
                  const int* __restrict__ kv_len, const float* __restrict__ xs, const float* __restrict__ tau,
-                 const int* __restrict__ list, const int* __restrict__ count, int* __restrict__ offs,
-                 float* __restrict__ part, WsHeader* __restrict__ hdr, DecodeGeom g, int split, float e_pow, float sm2) {
+                 const int* __restrict__ list, const int* __restrict__ count, float* __restrict__ part,
+                 WsHeader* __restrict__ hdr, DecodeGeom g, int split, float e_pow, float sm2) {
     using L = Q8Layout<D>;
     using namespace sm100;
     constexpr int NT = D / 16;                       // 16-dim output tiles
@@ -117,11 +118,10 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();                                     // after the wait: the merge may read the lists at once
     // the barriers are visible after list_share's barriers
     const ListShare sh = list_share<(kQ8Warps + 1) * 32>(count, g.B * g.Hkv, cta, (int)gridDim.x, kQ8Per, share_sh);
-    if (tid == 0 && cta == 0) offs[g.B * g.Hkv] = sh.U;   // for the merge
     if (sh.lo >= sh.hi) return;                        // whole CTA: nothing listed for it
     volatile int* abort_flag = &abort_sh;
 
@@ -139,7 +139,6 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             o1 = bg == sh.first ? sh.o_end : o0 + __ldcg(count + bg);
             if (o1 <= pos) continue;
             const int e_end = min(sh.hi, o1) - o0;
-            if (pos == o0 && lane == 0) offs[bg] = o0;
             const int b = bg / g.Hkv, kvh = bg % g.Hkv, row0 = bg / split * g.Tmax;
             const int bt = (kv_len[b] - 1) / kBlock;
             const size_t qrow = (size_t)b * g.Hq + (size_t)kvh * g.G + (hl < g.G ? hl : 0);
@@ -431,63 +430,38 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 }
 
 // One CTA of four warps per query head merges the partials of its group: every warp that had a
-// unit of the group left one.
+// unit of the group left one.  Where they lie follows from the lists' lengths, which are there before
+// the attention ends; then the statistics and the first outputs are loaded together.
 template <int D>
 __global__ void __launch_bounds__(128)
-decode_q8_combine_kernel(const int* __restrict__ count, const int* __restrict__ offs, const float* __restrict__ part,
-                         __nv_bfloat16* __restrict__ out, DecodeGeom g, int nctas) {
+decode_q8_combine_kernel(const int* __restrict__ count, const float* __restrict__ part, __nv_bfloat16* __restrict__ out,
+                         DecodeGeom g, int nctas) {
     constexpr uint32_t kRow = Q8Layout<D>::kRow;
-    constexpr int DPL = D / 32;
+    constexpr int DPL = D / 32, KB = 8;                // KB: pieces whose loads are in flight together
     __shared__ float wt_sh[kDecodeMaxCtas * kQ8Warps], red[2][4], os[4][D];
+    __shared__ int place_sh[8];
     const int bh = blockIdx.x, b = bh / g.Hq, h = bh % g.Hq, bg = b * g.Hkv + h / g.G, hl = h % g.G;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_wait();
-    const int n = count[bg];
-    if (n == 0) return;                                // no keys: the select pass wrote zeros
-    const int U = offs[g.B * g.Hkv], o0 = offs[bg], nC = split_ctas(U, nctas, kQ8Per);
-    const int c0 = dt_cta_of(o0, U, nC), c1 = dt_cta_of(o0 + n - 1, U, nC);
-    const int np = (c1 - c0 + 1) * kQ8Warps;
+    const ListPlace at = list_place<128>(count, g.B * g.Hkv, bg, place_sh);
+    const ListSplit sp(at.U, nctas, kQ8Per);
+    int c0 = 0, np = 0;
+    if (at.n > 0) {
+        c0 = sp.cta_of(at.o0);
+        np = (sp.cta_of(at.o0 + at.n - 1) - c0 + 1) * kQ8Warps;
+    }
     const float* p = part + ((size_t)(c0 + bg) * kQ8Warps * g.G + hl) * kRow;
     const size_t step = (size_t)g.G * kRow;
-    // whether warp i % kQ8Warps of CTA c0 + i / kQ8Warps had one of the group's units
-    auto there = [&](int i) {
-        const int c = c0 + i / kQ8Warps, w = i % kQ8Warps;
-        const int lo = (int)((long long)U * c / nC), hi = (int)((long long)U * (c + 1) / nC);
-        const int u0 = 2 * (max(lo, o0) - lo), u1 = 2 * (min(hi, o0 + n) - lo);
-        return u0 + (w - u0 % kQ8Warps + kQ8Warps) % kQ8Warps < u1;
-    };
-    float MA = -INFINITY, MB = -INFINITY;
+    // 1 where warp i % kQ8Warps of CTA c0 + i / kQ8Warps had one of the group's units
     for (int i = tid; i < np; i += 128) {
-        const bool have = there(i);
-        const float4 v = have ? __ldcg(reinterpret_cast<const float4*>(p + i * step)) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-        MA = fmaxf(MA, v.x);
-        MB = fmaxf(MB, v.z);
-        wt_sh[i] = have ? 1.f : 0.f;
+        const int c = c0 + i / kQ8Warps, w = i % kQ8Warps, lo = sp.lo(c), hi = sp.lo(c + 1);
+        const int u0 = 2 * (max(lo, at.o0) - lo), u1 = 2 * (min(hi, at.o0 + at.n) - lo);
+        wt_sh[i] = u0 + (w - u0 % kQ8Warps + kQ8Warps) % kQ8Warps < u1 ? 1.f : 0.f;
     }
-    MA = warp_max(MA);
-    MB = warp_max(MB);
-    if (lane == 0) { red[0][warp] = MA; red[1][warp] = MB; }
     __syncthreads();
-    MA = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    MB = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
-    const float ua = MA == -INFINITY ? 0.f : MA, ub = MB == -INFINITY ? 0.f : MB;
-    float den = 0.f;
-    for (int i = tid; i < np; i += 128) {
-        if (wt_sh[i] == 0.f) continue;                 // nothing was left there
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(p + i * step));
-        den = fmaf(v.y, exp2f(v.x - ua), den);
-        wt_sh[i] = exp2f(v.z - ub);
-    }
-    den = warp_sum(den);
-    __syncthreads();
-    if (lane == 0) red[0][warp] = den;
-    __syncthreads();
-    float acc[DPL];
-#pragma unroll
-    for (int d = 0; d < DPL; ++d) acc[d] = 0.f;
-    constexpr int KB = 8;                              // pieces whose loads are in flight together
-    for (int i0 = warp; i0 < np; i0 += 4 * KB) {
-        float v[KB][DPL];
+    pdl_wait();
+    if (np == 0) return;                               // no keys: the select pass wrote zeros
+    float v[KB][DPL];
+    auto load = [&](int i0) {
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
             const int i = i0 + 4 * k;
@@ -504,6 +478,39 @@ decode_q8_combine_kernel(const int* __restrict__ count, const int* __restrict__ 
                 }
             }
         }
+    };
+    auto stats = [&](int i) {
+        return i < np && wt_sh[i] != 0.f ? __ldcg(reinterpret_cast<const float4*>(p + i * step)) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    };
+    const float4 first = stats(tid);
+    load(warp);
+    float MA = first.x, MB = first.z;
+    for (int i = tid + 128; i < np; i += 128) {
+        const float4 s = stats(i);
+        MA = fmaxf(MA, s.x);
+        MB = fmaxf(MB, s.z);
+    }
+    MA = warp_max(MA);
+    MB = warp_max(MB);
+    if (lane == 0) { red[0][warp] = MA; red[1][warp] = MB; }
+    __syncthreads();                                   // also: every warp has read its flags
+    MA = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    MB = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+    const float ua = MA == -INFINITY ? 0.f : MA, ub = MB == -INFINITY ? 0.f : MB;
+    float den = first.y * exp2f(first.x - ua);         // 0 where nothing was left (exp2 of -inf)
+    for (int i = tid + 128; i < np; i += 128) {
+        const float4 s = stats(i);
+        den = fmaf(s.y, exp2f(s.x - ua), den);
+        if (wt_sh[i] != 0.f) wt_sh[i] = exp2f(s.z - ub);
+    }
+    if (tid < np && wt_sh[tid] != 0.f) wt_sh[tid] = exp2f(first.z - ub);
+    den = warp_sum(den);
+    __syncthreads();
+    if (lane == 0) red[0][warp] = den;
+    float acc[DPL];
+#pragma unroll
+    for (int d = 0; d < DPL; ++d) acc[d] = 0.f;
+    for (int i0 = warp;;) {
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
             const int i = i0 + 4 * k;
@@ -511,6 +518,9 @@ decode_q8_combine_kernel(const int* __restrict__ count, const int* __restrict__ 
 #pragma unroll
             for (int d = 0; d < DPL; ++d) acc[d] = fmaf(v[k][d], wk, acc[d]);
         }
+        i0 += 4 * KB;
+        if (i0 >= np) break;
+        load(i0);
     }
 #pragma unroll
     for (int d = 0; d < DPL; ++d) os[warp][lane * DPL + d] = acc[d];
@@ -537,14 +547,13 @@ static cudaError_t launch_attn(const void* q, const void* kc, const void* vc, co
                            static_cast<const uint8_t*>(ks), static_cast<const uint8_t*>(vs), kv_len,
                            reinterpret_cast<const float*>(ws + g.off_x), reinterpret_cast<const float*>(ws + g.off_tau),
                            reinterpret_cast<const int*>(ws + g.off_list), reinterpret_cast<const int*>(ws + g.off_count),
-                           reinterpret_cast<int*>(ws + g.off_offs), reinterpret_cast<float*>(ws + g.off_part),
+                           reinterpret_cast<float*>(ws + g.off_part),
                            reinterpret_cast<WsHeader*>(ws), g, gq.split, 1.0f / (alpha - 1.0f),
                            1.4426950408889634f / sqrtf((float)D));
     if (e != cudaSuccess) return e;
     const PdlConfig cc(g.B * g.Hq, 128, 0, stream);
     e = cudaLaunchKernelEx(&cc.cfg, decode_q8_combine_kernel<D>, reinterpret_cast<const int*>(ws + g.off_count),
-                           reinterpret_cast<const int*>(ws + g.off_offs), reinterpret_cast<const float*>(ws + g.off_part),
-                           static_cast<__nv_bfloat16*>(out), g, nctas);
+                           reinterpret_cast<const float*>(ws + g.off_part), static_cast<__nv_bfloat16*>(out), g, nctas);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

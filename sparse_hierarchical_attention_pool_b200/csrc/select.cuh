@@ -17,9 +17,15 @@ struct WarpRow {
     // buf: cap floats of this warp
     __device__ __forceinline__ void load(const float* row, float* buf, int cap, int ln, int count) {
         s = buf; p = row; lane = ln; n = count; ns = min(n, cap);
-        for (int j = lane; j < ns; j += 32) cp_async4(buf + j, row + j);
+        if (((reinterpret_cast<size_t>(row) & 15) | (cap & 3)) == 0) {
+            // whole chunks: up to 3 values past n, which no pass reads
+            for (int j = 4 * lane; j < ns; j += 128) cp_async16(buf + j, row + j, 16);
+        } else {
+            for (int j = lane; j < ns; j += 32) cp_async4(buf + j, row + j);
+        }
         cp_async_commit();
-        cp_async_wait<0>();                            // a lane reads only what it copied
+        cp_async_wait<0>();
+        __syncwarp();
     }
     template <class F>
     __device__ __forceinline__ void each(F&& f) const {
@@ -28,10 +34,11 @@ struct WarpRow {
         for (; j < ns; j += 32) f(j, s[j]);
         for (; j < n; j += 32) f(j, p[j]);
     }
-    __device__ __forceinline__ float max() const {
+    // largest of the lane's values
+    __device__ __forceinline__ float lane_max() const {
         float m = -INFINITY;
         each([&](int, float v) { m = fmaxf(m, v); });
-        return warp_max(m);
+        return m;
     }
     // Bitmap of the values above t: calls f(k, word) for every word k with a bit set, on the lane
     // that holds it (a ballot over the lanes is a word; 32 words are gathered before their lanes
@@ -204,18 +211,68 @@ __device__ __forceinline__ float lane_start_t(float y, float alpha) {
     }
     return sv.lo;
 }
-__device__ __forceinline__ float lane_start(const WarpRow& xr, float m, float alpha) {
-    float y = -INFINITY;
-    xr.each([&](int, float v) { y = fmaxf(y, v); });
-    y -= m;
+// y: the lane's largest value less the row's
+__device__ __forceinline__ float lane_start(float y, float alpha) {
     return alpha == 1.5f ? lane_start_t<1>(y, alpha) : alpha == 2.0f ? lane_start_t<2>(y, alpha) : lane_start_t<0>(y, alpha);
 }
 
 // CTAs that share U blocks: at most `grid`, and (per > 1) at least `per` blocks each where U
 // allows, so that short lists are not cut into pieces whose merge costs more than they save.
-__host__ __device__ inline int split_ctas(long long U, int grid, int per) {
-    const long long n = per > 1 ? (U + per - 1) / per : U;
-    return (int)(n < (long long)grid ? n : (long long)grid);
+__host__ __device__ inline int split_ctas(int U, int grid, int per) {
+    const unsigned n = ((unsigned)U + per - 1) / per;
+    return n < (unsigned)grid ? (int)n : grid;
+}
+
+// The ranges [U c / n, U (c + 1) / n) of the n CTAs that share U > 0 entries, in 32-bit arithmetic
+// (n <= kDecodeMaxCtas; a 64-bit division costs a few hundred cycles where a step has none to lose).
+struct ListSplit {
+    unsigned U, n, q, r;
+    __device__ __forceinline__ ListSplit(int U_, int grid, int per) : U((unsigned)U_), n((unsigned)split_ctas(U_, grid, per)) {
+        q = n ? U / n : 0u;
+        r = U - q * n;
+    }
+    __device__ __forceinline__ int lo(int c) const { return (int)(q * (unsigned)c + (n ? r * (unsigned)c / n : 0u)); }
+    // the CTA whose range holds position pos: an estimate (relative error below 2^-21, so at most one
+    // off), put right
+    __device__ __forceinline__ int cta_of(int pos) const {
+        int c = min((int)n - 1, (int)((float)pos / (float)U * (float)n));
+        while (c > 0 && lo(c) > pos) --c;
+        while (c + 1 < (int)n && lo(c + 1) <= pos) ++c;
+        return c;
+    }
+};
+
+// CTA c's range and the number of CTAs.  Not inlined: in line, its divisions cost the attention kernels
+// registers to the end (240 bytes of spills a thread in the 8-bit tree variant).
+static __device__ __noinline__ int3 cta_range(int U, int grid, int per, int c) {
+    const ListSplit sp(U, grid, per);
+    return make_int3(sp.lo(c), sp.lo(c + 1), (int)sp.n);
+}
+
+// Where list x lies in the concatenation, from the lists' lengths: its first entry, its length, and the
+// entries of all.  All NT threads of the CTA call it; sh: NT / 16 ints.
+struct ListPlace {
+    int U, o0, n;
+};
+template <int NT>
+__device__ __forceinline__ ListPlace list_place(const int* count, int lists, int x, int* sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int all = 0, before = 0;
+    for (int i = tid; i < lists; i += NT) {
+        const int c = __ldcg(count + i);
+        all += c;
+        before += i < x ? c : 0;
+    }
+    ListPlace r;
+    r.n = __ldcg(count + x);
+    all = warp_sum_int(all);
+    before = warp_sum_int(before);
+    if (lane == 0) { sh[warp] = all; sh[NT / 32 + warp] = before; }
+    __syncthreads();
+    r.U = r.o0 = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) { r.U += sh[w]; r.o0 += sh[NT / 32 + w]; }
+    return r;
 }
 
 // A CTA's share of the concatenated lists, from their lengths alone: U entries in all, nC CTAs
@@ -251,11 +308,12 @@ __device__ __forceinline__ ListShare list_share(const int* count, int lists, int
         if (w < warp) pre += sh[w];
         r.U += sh[w];
     }
-    r.nC = split_ctas(r.U, grid, per);
+    const int3 range = cta_range(r.U, grid, per, cta);
+    r.nC = range.z;
     r.lo = r.hi = 0;
     if (cta < r.nC) {
-        r.lo = (int)((long long)r.U * cta / r.nC);
-        r.hi = (int)((long long)r.U * (cta + 1) / r.nC);
+        r.lo = range.x;
+        r.hi = range.y;
     }
     if (r.lo < r.hi && r.lo >= pre && r.lo < pre + sum) {
         // one thread's lists hold the first entry

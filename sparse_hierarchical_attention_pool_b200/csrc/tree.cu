@@ -96,12 +96,18 @@ __device__ __forceinline__ void tree_score_chunk(const __nv_bfloat16* q, const f
 template <int D, bool Q8>
 __global__ void __launch_bounds__(128)
 tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
-    __shared__ int par_s[kMaxNodes], dep_s[kMaxNodes];
-    __shared__ float path[kMaxNodes][D], tail_s[D];
+    constexpr int TPR = D / 4, NR = 128 / TPR;                      // threads of 4 dims for a row, rows at once
+    __shared__ int par_s[kMaxNodes];
+    constexpr int KR = D + 8;                                       // a row of keys: 16 bytes on, so that 8 rows' chunks miss each other's banks
+    __shared__ unsigned long long sum_s[kMaxNodes];
+    __shared__ __align__(16) __nv_bfloat16 key_s[kMaxNodes][KR];
+    __shared__ __align__(16) float tail_s[NR][D], tot_s[D];
+    __shared__ unsigned in_s[kMaxNodes / 32];
     const int bg = blockIdx.x, b = bg / g.Hkv, tid = threadIdx.x;
     pdl_trigger();
     if (bg == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid < (int)sizeof(WsHeader) / 16)
         reinterpret_cast<uint4*>(w.hdr)[tid] = make_uint4(0u, 0u, 0u, 0u);
+    if (blockIdx.y == 0 && tid < g.N) par_s[tid] = a.parent[(size_t)b * g.N + tid];
     int L, nodes;
     const bool live = tree_live(a.kv_len, a.n_nodes, g, b, &L, &nodes);
     const int F = live ? L / kBlock : 0;
@@ -114,77 +120,112 @@ tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
     // the group's tiles start with nothing selected
     for (int i = tid; i < g.tiles_bg * g.nbw; i += 128) w.bits[(size_t)bg * g.tiles_bg * g.nbw + i] = 0u;
     for (int i = tid; i < g.tiles_bg; i += 128) w.tick[bg * g.tiles_bg + i] = 0;
+    // Some path may complete the open block (a path has at most `nodes` tokens): the draft's keys are on
+    // their way while the paths are walked.
+    const int r = live ? L % kBlock : 0;
+    const bool may_cross = r + nodes > kBlock;
+    if (may_cross) {
+        const auto* kd = static_cast<const __nv_bfloat16*>(a.k_draft) + (size_t)bg * g.N * D;
+        for (int i = tid; i < (nodes + 15) / 16 * 16 * (D / 8); i += 128) {
+            const int row = i / (D / 8), ch = i % (D / 8) * 8;
+            cp_async16(&key_s[row][ch], kd + (size_t)min(row, nodes - 1) * D + ch, row < nodes ? 16 : 0);   // zeros past the nodes
+        }
+    }
+    cp_async_commit();
     // every node walks up its path (parents come before children, so the walk ends); a parent
     // outside [-1, i) makes the node and its descendants invalid
-    for (int i = tid; i < nodes; i += 128) par_s[i] = a.parent[(size_t)b * g.N + i];
     __syncthreads();
-    if (tid < g.N) {
-        unsigned long long m = 0ull;
-        int dp = -1;
-        if (live && tid < nodes) {
-            int i = tid;
-            while (i >= 0) {
-                const int p = par_s[i];
-                if (p < -1 || p >= i) { m = 0ull; dp = -1; break; }
-                m |= 1ull << i;
-                ++dp;
-                i = p;
-            }
+    unsigned long long m = 0ull;
+    int dp = -1;
+    if (tid < nodes && live) {
+        int i = tid;
+        while (i >= 0) {
+            const int p = par_s[i];
+            if (p < -1 || p >= i) { m = 0ull; dp = -1; break; }
+            m |= 1ull << i;
+            ++dp;
+            i = p;
         }
-        dep_s[tid] = dp;
-        if (bg % g.Hkv == 0) { w.anc[(size_t)b * g.N + tid] = m; w.depth[(size_t)b * g.N + tid] = dp; }
     }
-    const int r = L % kBlock;
-    if (!__syncthreads_or(live && tid < g.N && r + dep_s[tid < g.N ? tid : 0] >= kBlock)) return;
-    // path[i] = the cached keys of the open block, and the path's tokens in it (r + depth < 64): all
-    // rows loaded at once, then one addition per node down the tree, a thread per dim
-    if (tid < D) tail_s[tid] = 0.f;
+    if (tid < g.N && bg % g.Hkv == 0) { w.anc[(size_t)b * g.N + tid] = m; w.depth[(size_t)b * g.N + tid] = dp; }
+    if (!__syncthreads_or(may_cross && r + dp >= kBlock)) return;
+    const int c = tid % TPR * 4, r0 = tid / TPR;
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+    const size_t row0 = (size_t)bg * g.Tmax + (L - r);
+#pragma unroll 16
+    for (int i = r0; i < r; i += NR) {
+        float f[4];
+        if constexpr (Q8) {
+            e4m3x4_to_float(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.k_cache) + (row0 + i) * D + c),
+                            scale_value(static_cast<const uint8_t*>(a.k_scale)[row0 + i]), f);
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.k_cache) + (row0 + i) * D + c);
+            const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+            const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+            f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t[k] += f[k];
+    }
+    // A path's sum: the cached keys of the open block and the path's tokens in it, those with
+    // r + depth < 64 (the first 64 - r of a path, so they are bits of its ancestor set).  All sums
+    // at once are one product of the 0 / 1 ancestor matrix and the keys (exact products, fp32 sums): a
+    // warp takes 16 nodes, in place of a walk of up to 64 dependent additions (4 us, now 1).
+    const unsigned in_w = __ballot_sync(0xffffffffu, dp >= 0 && r + dp < kBlock);
+    if (tid < kMaxNodes && (tid & 31) == 0) in_s[tid >> 5] = in_w;
+    *reinterpret_cast<float4*>(&tail_s[r0][c]) = make_float4(t[0], t[1], t[2], t[3]);
+    cp_async_wait<0>();
     __syncthreads();
-    const auto* kd = static_cast<const __nv_bfloat16*>(a.k_draft) + (size_t)bg * g.N * D;
-    for (int i = tid; i < nodes * (D / 8); i += 128) {
-        float f[8];
-        bf16x8_to_float(__ldg(reinterpret_cast<const uint4*>(kd) + i), f);
+    const unsigned long long in = in_s[0] | (unsigned long long)in_s[1] << 32;
+    if (tid < kMaxNodes) sum_s[tid] = m & in;
+    if (tid < D) {
+        float v = 0.f;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) path[i / (D / 8)][i % (D / 8) * 8 + c] = f[c];
+        for (int k = 0; k < NR; ++k) v += tail_s[k][tid];           // a fixed order
+        tot_s[tid] = v;
     }
-    {
-        // 4 dims per thread; D / 4 threads cover a row, the rows of the open block go round robin
-        constexpr int TPR = D / 4, NR = 128 / TPR;
-        const int c = tid % TPR * 4, r0 = tid / TPR;
-        const size_t row0 = (size_t)bg * g.Tmax + (L - r);
-        float t[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int i = r0; i < r; i += NR) {
-            float f[4];
-            if constexpr (Q8) {
-                e4m3x4_to_float(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.k_cache) + (row0 + i) * D + c),
-                                scale_value(static_cast<const uint8_t*>(a.k_scale)[row0 + i]), f);
-            } else {
-                const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.k_cache) + (row0 + i) * D + c);
-                const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-                const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-                f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
-            }
+    __syncthreads();
+    const int lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
+    if (warp * 16 >= nodes) return;
+    const int n0 = warp * 16 + g4, n1 = n0 + 8;
+    const unsigned long long a0 = sum_s[n0], a1 = sum_s[n1];
+    float acc[D / 8][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) t[k] += f[k];
-        }
-        // row groups add in a fixed order
-        for (int gq = 0; gq < NR; ++gq) {
-            if (r0 == gq)
+    for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tail_s[c + k] += t[k];
-            __syncthreads();
+        for (int k = 0; k < 4; ++k) acc[n][k] = 0.f;
+    unsigned odd = 0u;                                              // a key that is no number
+    for (int k0 = 0; k0 < nodes; k0 += 16) {
+        // two bits as two bf16: 1 or 0
+        auto pair = [&](unsigned long long bits, int k) { return ((unsigned)(bits >> k) & 1u) * 0x3f80u | ((unsigned)(bits >> (k + 1)) & 1u) * 0x3f800000u; };
+        const int k = k0 + 2 * t4;
+        const uint32_t af[4] = {pair(a0, k), pair(a1, k), pair(a0, k + 8), pair(a1, k + 8)};
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+            uint32_t bf[4];
+            ldsm_x4_t(bf[0], bf[1], bf[2], bf[3], smem_u32(&key_s[k0 + (lane & 15)][n * 16 + (lane >> 4) * 8]));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) odd |= __vcmpeq2(bf[q] & 0x7f807f80u, 0x7f807f80u);
+            mma_bf16(acc[2 * n], af, bf[0], bf[1]);
+            mma_bf16(acc[2 * n + 1], af, bf[2], bf[3]);
         }
     }
     float* dst = w.path + (size_t)bg * g.N * D;
-    if (tid < D) {
-        for (int i = 0; i < nodes; ++i) {
-            if (dep_s[i] < 0) continue;
-            const float up = par_s[i] >= 0 ? path[par_s[i]][tid] : tail_s[tid];
-            const float v = r + dep_s[i] < kBlock ? up + path[i][tid] : up;
-            path[i][tid] = v;
-            dst[(size_t)i * D + tid] = v;
-        }
+    if (__any_sync(0xffffffffu, odd != 0u)) {
+        // 0 times a key that is no number would reach nodes off its path: node by node
+        for (int i = warp * 16; i < min(nodes, warp * 16 + 16); ++i)
+            for (int e = lane; e < D; e += 32) {
+                float v = tot_s[e];
+                for (unsigned long long up = sum_s[i]; up; up &= up - 1) v += __bfloat162float(key_s[__ffsll((long long)up) - 1][e]);
+                dst[(size_t)i * D + e] = v;
+            }
+        return;
+    }
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+        const float2 v = *reinterpret_cast<const float2*>(&tot_s[n * 8 + 2 * t4]);
+        if (n0 < nodes) *reinterpret_cast<float2*>(dst + (size_t)n0 * D + n * 8 + 2 * t4) = make_float2(v.x + acc[n][0], v.y + acc[n][1]);
+        if (n1 < nodes) *reinterpret_cast<float2*>(dst + (size_t)n1 * D + n * 8 + 2 * t4) = make_float2(v.x + acc[n][2], v.y + acc[n][3]);
     }
 }
 
@@ -233,13 +274,14 @@ tree_select_kernel(TreeArgs a, TreeWork w, TreeGeom g, float alpha, float cx) {
                 float s = 0.f;
                 for (int c = lane; c < g.d; c += 32) s = fmaf(__bfloat162float(qr[c]), pr[c], s);
                 s = warp_sum(s) * (cx / kBlock);
-                if (lane == (F & 31)) xrow[F] = s;               // the lane that reads it below
+                if (lane == 0) xrow[F] = s;
+                __syncwarp();
             }
             int no_conv = 0, nsel = 0;
             WarpRow xr;
             xr.load(xrow, rows_sm + (size_t)warp * scap, scap, lane, n);
-            const float m = xr.max();
-            if (m > -INFINITY) t = row_tau(xr, m, alpha, &no_conv, nullptr, g.maxit, lane_start(xr, m, alpha));
+            const float y = xr.lane_max(), m = warp_max(y);
+            if (m > -INFINITY) t = row_tau(xr, m, alpha, &no_conv, nullptr, g.maxit, lane_start(y - m, alpha));
             nsel = xr.words(t, [&](int k, unsigned sel) { atomicOr(&w.bits[(size_t)tile * g.nbw + k], sel); });
             if (lane == 0) {
                 if (no_conv) atomicOr(&w.hdr->status, kStNoConverge);

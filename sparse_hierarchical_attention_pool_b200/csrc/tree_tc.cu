@@ -122,14 +122,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         if (warp == 11 && lane == 0) { prefetch_tmap(&tm_v); prefetch_tmap(&tm_vd); }
     }
     tc_fence_before();
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();                                               // after the wait: the merge may read the lists at once
     // its barriers also publish the set-up above
     const ListShare sh = list_share<NT>(w.count, g.tiles, cta, (int)gridDim.x, per, share_sh);
     tc_fence_after();
-    const long long U = sh.U;
-    const int nC = sh.nC;
-    if (cta == 0 && tid == 0) w.offs[g.tiles] = sh.U;
     const uint32_t tmem = tmem_sh;
     volatile int* abort_flag = &abort_sh;
     auto k_addr = [&](int st) { return base + L::off_k + (uint32_t)st * L::kTile; };
@@ -608,7 +605,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 tc_fence_before();
                 arrive(bar(B_PF + grp));
             }
-            if (tid == 0 && e0 == 0) w.offs[tile] = o0;          // for the merge of a split tile
             // ---- the two groups' states: (max, sum, output) of every row
             m_sh[grp][r] = m_run;
             l_sh[grp][r] = l_run;
@@ -626,7 +622,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 const float w0 = m0 == -INFINITY ? 0.f : exp2f(m0 - M), w1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
                 const float l0 = l_sh[0][r], l1 = l_sh[1][r];
                 const float den = (w0 > 0.f ? l0 * w0 : 0.f) + (w1 > 0.f ? l1 * w1 : 0.f);
-                const bool direct = dt_cta_of(o0, U, nC) == dt_cta_of(o1 - 1, U, nC);
+                // whether the tile lies in this CTA's range
+                const bool direct = sh.lo <= o0 && o1 <= sh.hi;
                 // partial of a tile: (max, sum) per row, then the outputs as [dims / 4][row][4], which
                 // the lanes of a warp (rows) write side by side
                 float* pr = w.part + ((size_t)cta + tile) * kTreeRows * (D + 4);
@@ -681,70 +678,105 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     if (tid == 0 && abort_sh) atomicOr(&w.hdr->status, kStWaitTimeout);
 }
 
-// Merges the partials of a tile that several CTAs share: a CTA takes 1024 / D rows, a warp their
-// weights (lanes over the pieces), then a thread four dims of a row, the lanes side by side in
-// the partials' [dims / 4][row] order and eight pieces in flight.
-template <int D>
+// Merges the partials of a tile that several CTAs share.  A CTA takes 1024 / (D PG) rows: a warp
+// makes the weights of a row's pieces (lanes over the pieces), a thread sums four dims of a row over
+// every PG-th piece, eight of them in flight, and the PG sums are added in order.  The lanes of a
+// warp read side by side in the partials' [dims / 4][row] order.  Which pieces there are follows from the
+// lists' lengths, which are there before the attention ends.
+template <int D, int PG>
 __global__ void __launch_bounds__(256)
 tree_combine_kernel(TreeArgs a, TreeWork w, TreeGeom g, int nctas, int per) {
-    constexpr int RPC = 1024 / D, kPerTile = kTreeRows / RPC;
+    constexpr int RPC = 1024 / (D * PG), RW = (RPC + 7) / 8, KB = 8;   // RW: rows whose weights a warp makes
     __shared__ float wt_sh[RPC][kDecodeMaxCtas], inv_sh[RPC];
-    const int tile = blockIdx.x / kPerTile, r0 = (blockIdx.x % kPerTile) * RPC;
+    __shared__ float4 sum_sh[PG][256 / PG];
+    __shared__ int place_sh[16];
+    const int per_tile = (min(g.R, kTreeRows) + RPC - 1) / RPC;
+    const int tile = blockIdx.x / per_tile, r0 = (blockIdx.x % per_tile) * RPC;
     const int bg = tile / g.tiles_bg, b = bg / g.Hkv, row0 = (tile % g.tiles_bg) * kTreeRows + r0;
-    if (row0 >= g.R) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_wait();
-    const int n = w.count[tile];
-    if (n == 0) return;
-    const long long U = w.offs[g.tiles];
-    const int o0 = w.offs[tile], o1 = o0 + n;
-    const int nC = split_ctas(U, nctas, per);
-    const int c0 = dt_cta_of(o0, U, nC), c1 = dt_cta_of(o1 - 1, U, nC);
-    if (c0 == c1) return;
+    const ListPlace at = list_place<256>(w.count, g.tiles, tile, place_sh);
+    const ListSplit sp(at.U, nctas, per);
+    int c0 = 0, np = 1;
+    if (at.n > 0) {
+        c0 = sp.cta_of(at.o0);
+        np = sp.cta_of(at.o0 + at.n - 1) - c0 + 1;
+    }
     int len, nodes;
-    if (!tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes)) return;
+    const bool live = tree_live(a.kv_len, a.n_nodes, g, b, &len, &nodes);
+    bool there[RW];
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+        const int row = row0 + warp + 8 * k, node = row % g.N;
+        there[k] = warp + 8 * k < RPC && row < g.R && node < nodes && __ldcg(w.anc + (size_t)b * g.N + node) != 0ull;
+    }
+    pdl_wait();
+    if (np == 1 || !live || row0 >= g.R) return;                 // finished by one CTA, or nothing to do
     const float* p = w.part + ((size_t)c0 + tile) * kTreeRows * (D + 4);
     const size_t step = (size_t)kTreeRows * (D + 4);
-    const int np = c1 - c0 + 1;
-    for (int rr = warp; rr < RPC; rr += 8) {
-        const int row_g = row0 + rr, node = row_g % g.N;
-        if (row_g >= g.R || node >= nodes || !w.anc[(size_t)b * g.N + node]) {
-            if (lane == 0) inv_sh[rr] = -1.f;                    // no such row, or none to merge
-            continue;
+    const int rr = tid % RPC, c4 = tid / RPC % (D / 4), pg = tid / (256 / PG);
+    const float* po = p + 4 * kTreeRows + ((size_t)c4 * kTreeRows + r0 + rr) * 4;
+    float4 v[KB];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+            if (i0 + k * PG < np) v[k] = __ldcg(reinterpret_cast<const float4*>(po + (i0 + k * PG) * step));
+    };
+    load(pg);
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+        const int rw = warp + 8 * k;
+        if (rw >= RPC) break;
+        float den = -1.f;                                        // no such row, or none to merge
+        if (there[k]) {
+            const float* ph = p + 2 * (r0 + rw);
+            auto stats = [&](int i) { return i < np ? __ldcg(reinterpret_cast<const float2*>(ph + i * step)) : make_float2(-INFINITY, 0.f); };
+            const float2 first = stats(lane);
+            float M = first.x;
+            for (int i = lane + 32; i < np; i += 32) M = fmaxf(M, stats(i).x);
+            M = warp_max(M);
+            den = 0.f;
+            for (int i = lane; i < np; i += 32) {
+                const float2 ml = i < 32 ? first : stats(i);
+                const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+                wt_sh[rw][i] = wt;
+                den = fmaf(ml.y, wt, den);
+            }
+            den = warp_sum(den);
         }
-        const float* ph = p + 2 * (r0 + rr);
-        float M = -INFINITY, den = 0.f;
-        for (int i = lane; i < np; i += 32) M = fmaxf(M, __ldcg(ph + i * step));
-        M = warp_max(M);
-        for (int i = lane; i < np; i += 32) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(ph + i * step));
-            const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-            wt_sh[rr][i] = wt;
-            den = fmaf(ml.y, wt, den);
-        }
-        den = warp_sum(den);
-        if (lane == 0) inv_sh[rr] = 1.0f / den;
+        if (lane == 0) inv_sh[rw] = den < 0.f ? -1.f : 1.0f / den;
     }
     __syncthreads();
-    const int rr = tid % RPC, c4 = tid / RPC;
     const float inv = inv_sh[rr];
-    if (inv < 0.f) return;
-    const float* po = p + 4 * kTreeRows + ((size_t)c4 * kTreeRows + r0 + rr) * 4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int KB = 8;
-    for (int i0 = 0; i0 < np; i0 += KB) {
-        float4 v[KB];
+    if (!(inv < 0.f)) {
+        for (int i0 = pg;;) {
 #pragma unroll
-        for (int k = 0; k < KB; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(po + min(i0 + k, np - 1) * step));
-#pragma unroll
-        for (int k = 0; k < KB; ++k) {
-            const float wt = i0 + k < np ? wt_sh[rr][i0 + k] : 0.f;
-            acc.x = fmaf(v[k].x, wt, acc.x);
-            acc.y = fmaf(v[k].y, wt, acc.y);
-            acc.z = fmaf(v[k].z, wt, acc.z);
-            acc.w = fmaf(v[k].w, wt, acc.w);
+            for (int k = 0; k < KB; ++k) {
+                const int i = i0 + k * PG;
+                if (i < np) {
+                    const float wt = wt_sh[rr][i];
+                    acc.x = fmaf(v[k].x, wt, acc.x);
+                    acc.y = fmaf(v[k].y, wt, acc.y);
+                    acc.z = fmaf(v[k].z, wt, acc.z);
+                    acc.w = fmaf(v[k].w, wt, acc.w);
+                }
+            }
+            i0 += KB * PG;
+            if (i0 >= np) break;
+            load(i0);
         }
     }
+    if constexpr (PG > 1) {
+        sum_sh[pg][tid % (256 / PG)] = acc;
+        __syncthreads();
+        if (pg > 0) return;
+#pragma unroll
+        for (int k = 1; k < PG; ++k) {
+            const float4 o = sum_sh[k][tid];
+            acc.x += o.x; acc.y += o.y; acc.z += o.z; acc.w += o.w;
+        }
+    }
+    if (inv < 0.f) return;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + ((size_t)bg * g.R + row0 + rr) * D + c4 * 4) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
@@ -766,8 +798,14 @@ static cudaError_t launch_t(const TreeArgs& a, const TreeWork& w, const TreeGeom
     const PdlConfig ca(nctas, kTtThreads<Q8>, sm, stream);
     e = cudaLaunchKernelEx(&ca.cfg, tree_attn_kernel<D, Q8>, tk, tv, tkd, tvd, a, w, g, e_pow, sm2, per);
     if (e != cudaSuccess) return e;
-    const PdlConfig cc((unsigned)g.tiles * (kTreeRows * D / 1024), 256, 0, stream);
-    e = cudaLaunchKernelEx(&cc.cfg, tree_combine_kernel<D>, a, w, g, nctas, per);
+    // few tiles: long lists of pieces and few CTAs, so four threads share a sum (one of 128 rows and 37
+    // pieces a row: 14 us without); many tiles have a few pieces each
+    const int rows = g.R < kTreeRows ? g.R : kTreeRows;
+    const bool wide = (long long)g.tiles * rows * D / 1024 <= nctas;
+    const int rpc = 1024 / D / (wide ? 4 : 1);
+    const PdlConfig cc((unsigned)g.tiles * ((rows + rpc - 1) / rpc), 256, 0, stream);
+    e = wide ? cudaLaunchKernelEx(&cc.cfg, tree_combine_kernel<D, 4>, a, w, g, nctas, per)
+             : cudaLaunchKernelEx(&cc.cfg, tree_combine_kernel<D, 1>, a, w, g, nctas, per);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
