@@ -462,8 +462,9 @@ DASH_API size_t dash_decode_tree_workspace_size(int B, int Hq, int Hkv, int N, i
  *   out      device bf16 [B, Hq, N, d]
  * Nodes of a sequence with kv_len[b] outside its range, nodes whose parent lies outside
  * [-1, i), and their descendants get zero.  At most 32 query heads per KV head;
- * B * Hkv * Tmax < 2^31.  Cached rows before kv_len[b] and the draft rows of the nodes must be finite: a
- * non-finite value can reach every row of its KV group.
+ * B * Hkv * Tmax < 2^31.  A drafted key that is no finite number reaches its node and that node's
+ * descendants alone; values, and cached keys, that are not finite can reach every row of their
+ * sequence and KV group, as they reach every head of a group in dash_decode.
  */
 DASH_API int dash_decode_tree(const void* q, const void* k_draft, const void* v_draft, const int* parent,
                               const int* n_nodes, const void* k_cache, const void* v_cache, const float* ksum,

@@ -226,7 +226,7 @@ struct TreeGeom {
     int lcap;                        // list entries per tile: the full blocks, the open one, the tree
     int nbw;                         // 32-bit words of a tile's selection bitmap
     int maxit;
-    size_t off_x, off_tau, off_anc, off_depth, off_path, off_bits, off_tick, off_list, off_count, off_part,
+    size_t off_x, off_tau, off_anc, off_depth, off_path, off_bits, off_tick, off_list, off_count, off_offs, off_part,
         total;
 };
 
@@ -254,6 +254,7 @@ inline bool make_tree_geom(int B, int Hq, int Hkv, int N, int Tmax, int d, TreeG
     g->off_tick = off;  off = align256(off + tiles * sizeof(int));
     g->off_list = off;  off = align256(off + tiles * g->lcap * sizeof(int));
     g->off_count = off; off = align256(off + tiles * sizeof(int));
+    g->off_offs = off;  off = align256(off + (tiles + 1) * sizeof(int));
     // partial (max, sum, padding to 16 bytes, output) per row of a (CTA + tile) slot
     g->off_part = off;  off = align256(off + (tiles + kDecodeMaxCtas) * kTreeRows * (d + 4) * sizeof(float));
     g->total = off;

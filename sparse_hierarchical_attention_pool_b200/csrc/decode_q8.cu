@@ -94,8 +94,8 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 2)
 decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vs,
                  const int* __restrict__ kv_len, const float* __restrict__ xs, const float* __restrict__ tau,
-                 const int* __restrict__ list, const int* __restrict__ count, float* __restrict__ part,
-                 WsHeader* __restrict__ hdr, DecodeGeom g, int split, float e_pow, float sm2) {
+                 const int* __restrict__ list, const int* __restrict__ count, int* __restrict__ offs,
+                 float* __restrict__ part, WsHeader* __restrict__ hdr, DecodeGeom g, int split, float e_pow, float sm2) {
     using L = Q8Layout<D>;
     using namespace sm100;
     constexpr int NT = D / 16;                       // 16-dim output tiles
@@ -122,6 +122,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     pdl_trigger();                                     // after the wait: the merge may read the lists at once
     // the barriers are visible after list_share's barriers
     const ListShare sh = list_share<(kQ8Warps + 1) * 32>(count, g.B * g.Hkv, cta, (int)gridDim.x, kQ8Per, share_sh);
+    if (tid == 0 && cta == 0) offs[g.B * g.Hkv] = sh.U;   // for the merge
     if (sh.lo >= sh.hi) return;                        // whole CTA: nothing listed for it
     volatile int* abort_flag = &abort_sh;
 
@@ -139,6 +140,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             o1 = bg == sh.first ? sh.o_end : o0 + __ldcg(count + bg);
             if (o1 <= pos) continue;
             const int e_end = min(sh.hi, o1) - o0;
+            if (pos == o0 && lane == 0) offs[bg] = o0;
             const int b = bg / g.Hkv, kvh = bg % g.Hkv, row0 = bg / split * g.Tmax;
             const int bt = (kv_len[b] - 1) / kBlock;
             const size_t qrow = (size_t)b * g.Hq + (size_t)kvh * g.G + (hl < g.G ? hl : 0);
@@ -434,15 +436,15 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 // the attention ends; then the statistics and the first outputs are loaded together.
 template <int D>
 __global__ void __launch_bounds__(128)
-decode_q8_combine_kernel(const int* __restrict__ count, const float* __restrict__ part, __nv_bfloat16* __restrict__ out,
-                         DecodeGeom g, int nctas) {
+decode_q8_combine_kernel(const int* __restrict__ count, const int* __restrict__ offs, const float* __restrict__ part,
+                         __nv_bfloat16* __restrict__ out, DecodeGeom g, int nctas) {
     constexpr uint32_t kRow = Q8Layout<D>::kRow;
     constexpr int DPL = D / 32, KB = 8;                // KB: pieces whose loads are in flight together
     __shared__ float wt_sh[kDecodeMaxCtas * kQ8Warps], red[2][4], os[4][D];
     __shared__ int place_sh[8];
     const int bh = blockIdx.x, b = bh / g.Hq, h = bh % g.Hq, bg = b * g.Hkv + h / g.G, hl = h % g.G;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const ListPlace at = list_place<128>(count, g.B * g.Hkv, bg, place_sh);
+    const ListPlace at = list_place<128>(count, offs, g.B * g.Hkv, bg, place_sh);
     const ListSplit sp(at.U, nctas, kQ8Per);
     int c0 = 0, np = 0;
     if (at.n > 0) {
@@ -547,13 +549,14 @@ static cudaError_t launch_attn(const void* q, const void* kc, const void* vc, co
                            static_cast<const uint8_t*>(ks), static_cast<const uint8_t*>(vs), kv_len,
                            reinterpret_cast<const float*>(ws + g.off_x), reinterpret_cast<const float*>(ws + g.off_tau),
                            reinterpret_cast<const int*>(ws + g.off_list), reinterpret_cast<const int*>(ws + g.off_count),
-                           reinterpret_cast<float*>(ws + g.off_part),
+                           reinterpret_cast<int*>(ws + g.off_offs), reinterpret_cast<float*>(ws + g.off_part),
                            reinterpret_cast<WsHeader*>(ws), g, gq.split, 1.0f / (alpha - 1.0f),
                            1.4426950408889634f / sqrtf((float)D));
     if (e != cudaSuccess) return e;
     const PdlConfig cc(g.B * g.Hq, 128, 0, stream);
     e = cudaLaunchKernelEx(&cc.cfg, decode_q8_combine_kernel<D>, reinterpret_cast<const int*>(ws + g.off_count),
-                           reinterpret_cast<const float*>(ws + g.off_part), static_cast<__nv_bfloat16*>(out), g, nctas);
+                           reinterpret_cast<const int*>(ws + g.off_offs), reinterpret_cast<const float*>(ws + g.off_part),
+                           static_cast<__nv_bfloat16*>(out), g, nctas);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -249,14 +249,23 @@ static __device__ __noinline__ int3 cta_range(int U, int grid, int per, int c) {
     return make_int3(sp.lo(c), sp.lo(c + 1), (int)sp.n);
 }
 
-// Where list x lies in the concatenation, from the lists' lengths: its first entry, its length, and the
-// entries of all.  All NT threads of the CTA call it; sh: NT / 16 ints.
+// Where list x lies in the concatenation: its first entry, its length, and the entries of all.  A merge
+// that starts before the attention has ended adds up the lists' lengths itself, so that nothing is
+// left to look up when it ends (16K tree: 14 us of merge, 4 with this and its loads together); from
+// kPlaceLists lists on, where every CTA's sums would weigh more, it takes what the attention leaves in
+// offs ([x] first entry, [lists] entries in all).  All NT threads of the CTA call it; sh: NT / 16 ints.
+constexpr int kPlaceLists = 1024;
 struct ListPlace {
     int U, o0, n;
 };
+__device__ __forceinline__ void pdl_wait();
 template <int NT>
-__device__ __forceinline__ ListPlace list_place(const int* count, int lists, int x, int* sh) {
+__device__ __forceinline__ ListPlace list_place(const int* count, const int* offs, int lists, int x, int* sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (lists >= kPlaceLists) {
+        pdl_wait();
+        return ListPlace{__ldcg(offs + lists), __ldcg(offs + x), __ldcg(count + x)};
+    }
     int all = 0, before = 0;
     for (int i = tid; i < lists; i += NT) {
         const int c = __ldcg(count + i);

@@ -265,7 +265,7 @@ tree_select_kernel(TreeArgs a, TreeWork w, TreeGeom g, float alpha, float cx) {
         float t = __int_as_float(0x7fc00000);
         if (live && dp >= 0) {
             const bool crossed = r + dp >= kBlock;
-            const int n = F + (crossed ? 1 : 0);
+            int n = F + (crossed ? 1 : 0);
             float* xrow = w.xs + row * g.cap;
             if (crossed) {
                 // the path completes the open block: its score from the mean of the block's 64 keys
@@ -274,6 +274,9 @@ tree_select_kernel(TreeArgs a, TreeWork w, TreeGeom g, float alpha, float cx) {
                 float s = 0.f;
                 for (int c = lane; c < g.d; c += 32) s = fmaf(__bfloat162float(qr[c]), pr[c], s);
                 s = warp_sum(s) * (cx / kBlock);
+                // a path with a key that is no number has no such score: NaN, which makes the row NaN in the
+                // attention, and no part of the threshold (it has no root then)
+                if (!(fabsf(s) < INFINITY)) { s = __int_as_float(0x7fc00000); n = F; }
                 if (lane == 0) xrow[F] = s;
                 __syncwarp();
             }

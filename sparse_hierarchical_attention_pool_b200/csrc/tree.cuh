@@ -17,6 +17,7 @@ struct TreeWork {
     float* path;                         // [B Hkv][N][D] sum of the open block's keys on a node's path
     unsigned* bits;                      // [tile][nbw] selected blocks
     int *tick, *list, *count;
+    int* offs;                           // [tile] first entry of split tiles; [tiles]: entries in all
     float* part;                         // [CTA + tile] partials of 128 rows (tree_tc.cu)
 };
 
@@ -32,6 +33,7 @@ inline TreeWork tree_work(const TreeGeom& g, char* ws) {
     w.tick = reinterpret_cast<int*>(ws + g.off_tick);
     w.list = reinterpret_cast<int*>(ws + g.off_list);
     w.count = reinterpret_cast<int*>(ws + g.off_count);
+    w.offs = reinterpret_cast<int*>(ws + g.off_offs);
     w.part = reinterpret_cast<float*>(ws + g.off_part);
     return w;
 }

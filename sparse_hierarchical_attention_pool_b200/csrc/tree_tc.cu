@@ -127,6 +127,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     // its barriers also publish the set-up above
     const ListShare sh = list_share<NT>(w.count, g.tiles, cta, (int)gridDim.x, per, share_sh);
     tc_fence_after();
+    if (cta == 0 && tid == 0) w.offs[g.tiles] = sh.U;
     const uint32_t tmem = tmem_sh;
     volatile int* abort_flag = &abort_sh;
     auto k_addr = [&](int st) { return base + L::off_k + (uint32_t)st * L::kTile; };
@@ -482,7 +483,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const float xF = crossed ? __ldcg(xr + F) : 0.f;
             float x0 = xval(j0);
             // log2 prior of the open block's keys: 1 while it is the own block
-            const float lpo = !crossed ? 0.f : (xF > tau_r ? e_pow * __log2f(xF - tau_r) : -INFINITY);
+            const float lpo = !crossed ? 0.f : xF > tau_r ? e_pow * __log2f(xF - tau_r) : xF == xF ? -INFINITY : xF;
             float m_run = -INFINITY, l_run = 0.f;
             for (int s = s0; s < n; s += 2) {
                 const int gs = gs0 + s, i2 = gs >> 1;
@@ -605,6 +606,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 tc_fence_before();
                 arrive(bar(B_PF + grp));
             }
+            if (tid == 0 && e0 == 0) w.offs[tile] = o0;          // for the merge of a split tile
             // ---- the two groups' states: (max, sum, output) of every row
             m_sh[grp][r] = m_run;
             l_sh[grp][r] = l_run;
@@ -694,7 +696,7 @@ tree_combine_kernel(TreeArgs a, TreeWork w, TreeGeom g, int nctas, int per) {
     const int tile = blockIdx.x / per_tile, r0 = (blockIdx.x % per_tile) * RPC;
     const int bg = tile / g.tiles_bg, b = bg / g.Hkv, row0 = (tile % g.tiles_bg) * kTreeRows + r0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const ListPlace at = list_place<256>(w.count, g.tiles, tile, place_sh);
+    const ListPlace at = list_place<256>(w.count, w.offs, g.tiles, tile, place_sh);
     const ListSplit sp(at.U, nctas, per);
     int c0 = 0, np = 1;
     if (at.n > 0) {

@@ -294,3 +294,81 @@ def test_decode_q8_many_sequences_split_over_ctas():
     close(out.float().cpu().reshape(-1, d), ref, float(vh.float().abs().max()), 1.5, 11)
     again, _ = da.dash_decode_q8(q.cuda(), *c, i32(lens), coarse_scale=0.05)
     assert torch.equal(out, again)                                   # the same every time
+
+
+@gpu
+def test_decode_q8_more_groups_than_a_merge_adds_up():
+    """From 1024 lists on, the merge looks its pieces up in what the attention left: sampled sequences,
+    empty ones among them, against the oracle."""
+    B, Hq, Hkv, T, d = 520, 4, 2, 128, 64
+    _, (q4, k, v) = inputs.make("16k", B=B, Hq=Hq, Hkv=Hkv, T=T, d=d, n_topics=2, seed=41)
+    c = filled(B, Hkv, T, d, k, v)
+    lens = [(37 * b) % 129 for b in range(B)]
+    kh, vh = (x.cpu() for x in da.dash_cache_read(*c[:4], T))
+    q = q4[:, :, 5].contiguous()
+    out, ws = da.dash_decode_q8(q.cuda(), *c, i32(lens), coarse_scale=0.05)
+    assert da.dash_get_device_status(ws) == 0
+    out = out.float().cpu()
+    some = [0, 1, 2, 7, 100, 255, 256, 511, 512, 518, 519] + [b for b in range(B) if lens[b] in (0, 64, 65, 128)][:8]
+    for b in some:
+        if lens[b] == 0:
+            assert bool((out[b] == 0).all())
+            continue
+        ref, _, _ = oracle.forward_rows(q[b], kh[b:b + 1], vh[b:b + 1], [(0, h, lens[b] - 1) for h in range(Hq)], Hq, 64, 1.5, 0.05)
+        close(out[b], ref, float(vh[b].float().abs().max()), 1.5, 11, f"sequence {b}")
+
+
+@gpu
+def test_decode_q8_rows_longer_than_the_shared_buffer():
+    """More blocks than a warp keeps in shared memory (1536): the rest of a row is read from memory."""
+    B, Hq, Hkv, T, d = 1, 2, 1, 131072, 64
+    _, (q4, k, v) = inputs.make("16k", B=B, Hq=Hq, Hkv=Hkv, T=T, d=d, n_topics=8, seed=43)
+    c = filled(B, Hkv, T, d, k, v)
+    kh, vh = (x.cpu() for x in da.dash_cache_read(*c[:4], T))
+    for L in (131072, 98305 + 40):
+        q = q4[:, :, L - 1].contiguous()
+        out, _ = da.dash_decode_q8(q.cuda(), *c, i32([L]), coarse_scale=0.05)
+        ref, _, _ = oracle.forward_rows(q.reshape(-1, d), kh, vh, [(0, h, L - 1) for h in range(Hq)], Hq, 64, 1.5, 0.05)
+        close(out.float().cpu().reshape(-1, d), ref, float(vh.float().abs().max()), 1.5, 11, f"L={L}")
+
+
+@gpu
+def test_decode_q8_two_calls_at_once_and_any_workspace():
+    """Calls on two streams with workspaces of their own, whatever the workspaces held, give what one
+    call alone gives, bit for bit."""
+    Hq, Hkv, d = 16, 2, 128
+    calls = []
+    for T, seed in ((8192, 61), (4096, 62)):
+        _, (q4, k, v) = inputs.make("16k", B=2, Hq=Hq, Hkv=Hkv, T=T, d=d, n_topics=8, seed=seed)
+        c = filled(2, Hkv, T, d, k, v)
+        q, lens = q4[:, :, 9].contiguous().cuda(), i32([T, T // 2 + 3])
+        alone, ws = da.dash_decode_q8(q, *c, lens, coarse_scale=0.05)
+        calls.append((q, c, lens, alone, torch.full_like(ws, 255), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        outs = []
+        for q, c, lens, _, ws, s in calls:
+            with torch.cuda.stream(s):
+                outs.append(da.dash_decode_q8(q, *c, lens, coarse_scale=0.05, workspace=ws)[0])
+        torch.cuda.synchronize()
+        for o, call in zip(outs, calls):
+            assert torch.equal(o, call[3])
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_and_read_at_the_largest_bf16_numbers(d):
+    """Rows whose magnitudes end at bf16's largest: held as 240 2^120 at most, and read back finite."""
+    x = torch.zeros(1, 1, 64, d)
+    top = float(torch.finfo(torch.bfloat16).max)
+    for i in range(64):
+        x[0, 0, i, i % d] = (-1) ** i * top * 2.0 ** (-i / 4)
+        x[0, 0, i, (i + 1) % d] = top / 3 if i % 2 else 2.0 ** -130
+    x = x.bfloat16()
+    c = junk_cache(1, 1, 64, d)
+    da.dash_cache_append(x.cuda(), (-x).cuda(), i32([0]), *c[:4], ksum=c[4], n=64)
+    want, scale = reference(x)
+    assert torch.equal(c[2].cpu(), scale)
+    k, v = da.dash_cache_read(*c[:4], 64)
+    assert torch.equal(k.double().cpu(), want) and torch.equal(v.double().cpu(), -want)
+    assert bool(torch.isfinite(k).all()) and float(k.abs().max()) <= 240 * 2.0 ** 120

@@ -215,3 +215,92 @@ def test_serving_steps_together():
         assert torch.equal(out_t, first[0]) and torch.equal(out_1, first[1])
     del g
     check()
+
+
+@gpu
+@pytest.mark.parametrize("q8", [False, True])
+def test_more_tiles_than_a_merge_adds_up(q8):
+    """From 1024 lists on, the merge looks its pieces up in what the attention left."""
+    B, Hq, Hkv, T, d, N = 520, 4, 2, 128, 64, 3
+    _, (_, k, v) = inputs.make("16k", B=B, Hq=Hq, Hkv=Hkv, T=T, d=d, n_topics=2, seed=101)
+    q, kd, vd = drafts(B, Hq, Hkv, N, d, 102, n_topics=2)
+    parent = [[-1, 0, 0] if b % 2 else [-1, 0, 1] for b in range(B)]
+    lens = [(37 * b) % 129 for b in range(B)]
+    got, kh, vh = run(q8, q, kd, vd, parent, k, v, lens, 1.5, junk=False)
+    got = got.float().cpu()
+    for b in [0, 1, 2, 7, 100, 255, 256, 511, 512, 518, 519] + [b for b in range(B) if lens[b] in (0, 63, 64, 128)][:8]:
+        ref = expected(q[b], kd[b], vd[b], parent[b], kh[b], vh[b], lens[b], 1.5)
+        close(got[b], ref, float(max(v[b].float().abs().max(), vd[b].float().abs().max())) * 1.1, 1.5, 8, f"sequence {b}")
+
+
+@gpu
+@pytest.mark.parametrize("q8", [False, True])
+def test_rows_longer_than_the_shared_buffer(q8):
+    """More blocks than a warp keeps in shared memory (1536), where the paths complete one more."""
+    B, Hq, Hkv, T, d, N = 1, 2, 1, 131072, 64, 3
+    _, (_, k, v) = inputs.make("16k", B=B, Hq=Hq, Hkv=Hkv, T=T, d=d, n_topics=8, seed=111)
+    q, kd, vd = drafts(B, Hq, Hkv, N, d, 112, n_topics=8)
+    for L in (131071, 98304 + 63):
+        got, kh, vh = run(q8, q, kd, vd, [[-1, 0, 1]], k, v, [L], 1.5, junk=False)
+        ref = expected(q[0], kd[0], vd[0], [-1, 0, 1], kh[0], vh[0], L, 1.5)
+        close(got[0].float().cpu(), ref, float(v.float().abs().max()) * 1.1, 1.5, 8, f"L={L}")
+
+
+@gpu
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_key_that_is_no_number_stays_on_its_paths(q8, bad):
+    """Node 5's key is no number: nodes that do not descend from it are right, in the open block (L = 10)
+    and where paths complete it (L = 61), whose summaries must not take it up either."""
+    B, Hq, Hkv, T, d, N = 2, 4, 2, 128, 64, 12
+    lens = [10, 61]
+    _, (_, k, v) = inputs.make("16k", B=B, Hq=Hq, Hkv=Hkv, T=T, d=d, n_topics=2, seed=121)
+    q, kd, vd = drafts(B, Hq, Hkv, N, d, 122, n_topics=2)
+    parent = [-1, 0, 1, 2, 3, 1, 5, 4, 7, 6, 8, 10]
+    others = [0, 1, 2, 3, 4, 7, 8, 10, 11]
+    kd[:, :, 5, 3] = bad
+    got, kh, vh = run(q8, q, kd, vd, [parent] * B, k, v, lens, 1.5)
+    clean = torch.where(torch.isfinite(kd), kd, torch.zeros_like(kd))
+    for b in range(B):
+        ref = expected(q[b], clean[b], vd[b], parent, kh[b], vh[b], lens[b], 1.5)
+        vmax = float(max(v[b].float().abs().max(), vd[b].float().abs().max())) * 1.1
+        close(got[b].float().cpu()[:, others], ref[:, others], vmax, 1.5, 8, f"L={lens[b]}")
+
+
+@gpu
+@pytest.mark.parametrize("q8", [False, True])
+def test_two_trees_at_once_from_graphs_with_any_workspace(q8):
+    """Two captured steps replayed on two streams, with workspaces of their own that held anything, give
+    what each gives alone, bit for bit; rows of another sequence's values that are NaN reach no one else."""
+    Hq, Hkv, d = 8, 2, 128
+    sides = []
+    for T, N, seed in ((4096, 16, 131), (2048, 40, 132)):
+        _, (_, k, v) = inputs.make("16k", B=2, Hq=Hq, Hkv=Hkv, T=T, d=d, n_topics=4, seed=seed)
+        q, kd, vd = (x.cuda() for x in drafts(2, Hq, Hkv, N, d, seed + 5))
+        par, lens = i32([random_tree(N, seed), list(range(-1, N - 1))]), i32([T, T - 70])
+        v[1, 0, 3] = float("nan")
+        if q8:
+            c = filled(2, Hkv, T, d, k, v)
+            args = (q, kd, vd, par, *c[:4], c[4], lens)
+            fn = da.dash_decode_tree_q8
+        else:
+            kc = k.cuda()
+            args = (q, kd, vd, par, kc, v.cuda(), da.dash_block_summary(kc), lens)
+            fn = da.dash_decode_tree
+        alone, ws = fn(*args, coarse_scale=CS)
+        assert bool(torch.isfinite(alone[0]).all())
+        ws, out = torch.full_like(ws, 255), torch.empty_like(alone)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            fn(*args, coarse_scale=CS, workspace=ws, out=out)
+        sides.append((graph, torch.cuda.Stream(), out, alone, args, ws))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for graph, stream, out, *_ in sides:
+            with torch.cuda.stream(stream):
+                out.zero_()
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, _, out, alone, *_ in sides:
+            assert torch.equal(out.view(torch.int16), alone.view(torch.int16))
