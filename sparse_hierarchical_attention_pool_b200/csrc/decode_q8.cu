@@ -249,6 +249,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             // B operand Q'^T: lane column g4 is the head; heads past G are zero
             uint4 w[D / 32];
             float amax = 0.f;
+            int bad = 0;                                 // an element that is no number: the head's logits are NaN
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 w[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -256,7 +257,11 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 float f[8];
                 bf16x8_to_float(w[c], f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]) < INFINITY ? fabsf(f[i]) : 0.f);
+                for (int i = 0; i < 8; ++i) {
+                    const bool fin = fabsf(f[i]) < INFINITY;
+                    amax = fmaxf(amax, fin ? fabsf(f[i]) : 0.f);
+                    bad |= !fin;
+                }
             }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
@@ -282,9 +287,12 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 }
             }
             // head h's factor sits on the lanes with g4 = h
+            const unsigned bads = __ballot_sync(0xffffffffu, bad);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                qf[i] = scalbnf(sm2, __shfl_sync(0xffffffffu, eq, (2 * t4 + i) * 4));
+                const unsigned lanes = 0xfu << ((2 * t4 + i) * 4);
+                const int e = __shfl_sync(0xffffffffu, eq, (2 * t4 + i) * 4);
+                qf[i] = bads & lanes ? __uint_as_float(0x7fc00000u) : scalbnf(sm2, e);
                 ma[i] = mb[i] = -INFINITY;
                 l_r[i] = 0.f;
             }

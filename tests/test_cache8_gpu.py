@@ -372,3 +372,31 @@ def test_append_and_read_at_the_largest_bf16_numbers(d):
     k, v = da.dash_cache_read(*c[:4], 64)
     assert torch.equal(k.double().cpu(), want) and torch.equal(v.double().cpu(), -want)
     assert bool(torch.isfinite(k).all()) and float(k.abs().max()) <= 240 * 2.0 ** 120
+
+
+@gpu
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_decode_q8_query_or_key_that_is_no_number(bad):
+    """A head whose query holds one is NaN; a key that holds one is NaN to the heads that attend its block.
+    The other heads are right."""
+    B, Hq, Hkv, T, d = 1, 4, 1, 256, 64
+    g = torch.Generator().manual_seed(5)
+    k, v = torch.zeros(B, Hkv, T, d), torch.randn(B, Hkv, T, d, generator=g)
+    for j in range(3):
+        k[:, :, 64 * j:64 * j + 64, j] = 4.0                         # block j points along dim j
+    q = torch.zeros(B, Hq, d)
+    for h in range(3):
+        q[:, h, h] = 8.0                                             # head h selects block h alone
+    q[:, 3, 0], q[:, 3, 9] = 8.0, bad
+    k, v, q = k.bfloat16(), v.bfloat16(), q.bfloat16()
+    c = filled(B, Hkv, T, d, k, v)
+    kh, vh = (x.cpu() for x in da.dash_cache_read(*c[:4], T))
+    ref, _, _ = oracle.forward_rows(q[0], kh, vh, [(0, h, T - 1) for h in range(3)], Hq, 64, 1.5, 1.0)
+    out, _ = da.dash_decode_q8(q.cuda(), *c, i32([T]), coarse_scale=1.0)
+    assert bool(out[0, 3].isnan().all())
+    close(out[0, :3].float().cpu(), ref, float(vh.float().abs().max()), 1.5, 11)
+    k[0, 0, 70, 5] = bad                                             # in block 1, whose summary stays as it was
+    da.dash_cache_append(k[:, :, 70:71].contiguous().cuda(), v[:, :, 70:71].contiguous().cuda(), i32([70]), *c[:4])
+    out, _ = da.dash_decode_q8(q.cuda(), *c, i32([T]), coarse_scale=1.0)
+    assert bool(out[0, 1].isnan().all())
+    close(out[0, [0, 2]].float().cpu(), ref[[0, 2]], float(vh.float().abs().max()), 1.5, 11)
