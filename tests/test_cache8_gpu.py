@@ -320,12 +320,12 @@ def test_decode_q8_more_groups_than_a_merge_adds_up():
 
 @gpu
 def test_decode_q8_rows_longer_than_the_shared_buffer():
-    """More blocks than a warp keeps in shared memory (1536): the rest of a row is read from memory."""
-    B, Hq, Hkv, T, d = 1, 2, 1, 131072, 64
+    """More blocks than a warp keeps in shared memory (4096): the rest of a row is read from memory."""
+    B, Hq, Hkv, T, d = 1, 2, 1, 262144 + 640, 64
     _, (q4, k, v) = inputs.make("16k", B=B, Hq=Hq, Hkv=Hkv, T=T, d=d, n_topics=8, seed=43)
     c = filled(B, Hkv, T, d, k, v)
     kh, vh = (x.cpu() for x in da.dash_cache_read(*c[:4], T))
-    for L in (131072, 98305 + 40):
+    for L in (T, 262145 + 40):
         q = q4[:, :, L - 1].contiguous()
         out, _ = da.dash_decode_q8(q.cuda(), *c, i32([L]), coarse_scale=0.05)
         ref, _, _ = oracle.forward_rows(q.reshape(-1, d), kh, vh, [(0, h, L - 1) for h in range(Hq)], Hq, 64, 1.5, 0.05)

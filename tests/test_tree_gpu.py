@@ -236,11 +236,11 @@ def test_more_tiles_than_a_merge_adds_up(q8):
 @gpu
 @pytest.mark.parametrize("q8", [False, True])
 def test_rows_longer_than_the_shared_buffer(q8):
-    """More blocks than a warp keeps in shared memory (1536), where the paths complete one more."""
-    B, Hq, Hkv, T, d, N = 1, 2, 1, 131072, 64, 3
+    """More blocks than a warp keeps in shared memory (4096), where the paths complete one more."""
+    B, Hq, Hkv, T, d, N = 1, 2, 1, 262144 + 640, 64, 3
     _, (_, k, v) = inputs.make("16k", B=B, Hq=Hq, Hkv=Hkv, T=T, d=d, n_topics=8, seed=111)
     q, kd, vd = drafts(B, Hq, Hkv, N, d, 112, n_topics=8)
-    for L in (131071, 98304 + 63):
+    for L in (T - 1, 262144 + 63):
         got, kh, vh = run(q8, q, kd, vd, [[-1, 0, 1]], k, v, [L], 1.5, junk=False)
         ref = expected(q[0], kd[0], vd[0], [-1, 0, 1], kh[0], vh[0], L, 1.5)
         close(got[0].float().cpu(), ref, float(v.float().abs().max()) * 1.1, 1.5, 8, f"L={L}")
