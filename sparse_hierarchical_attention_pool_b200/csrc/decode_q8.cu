@@ -49,8 +49,10 @@ constexpr int kQ8Keys = 32;          // keys per unit: a consumer's share of an 
 // the same two consumers: each waits for a stage only after it has used the entry before, and
 // the wait never meets a barrier that is still a phase behind.
 static_assert(kQ8Warps == 4 && kQ8Stages % 2 == 0, "a stage keeps its consumers");
-constexpr int kQ8Per = 6;            // list entries per CTA at least (16K, 2 KV heads: 4 entries 22.6 us a step, 6 21.2, 8 21.0;
-                                     // 5K of 64 dims: 19.7, 20.2, 20.8)
+// An entry takes a CTA as long as about 3 CTAs' pieces (4 warps each) take a merge (split_ctas).  With 6
+// entries a CTA always, lists of 1 to 6 blocks take 16.5 and 20.6 us a step against 14.4 and 16.5; with
+// 2 always, two lists of 117 blocks 25.2 us against 21.1.
+constexpr int kQ8Merge = 3;
 constexpr int kQ8PartHead = 4;       // floats of a partial before its output: mA, sum, mB, -
 constexpr float kWBits = 12.0f;      // weights reach 2^12: f16 then keeps terms down to 2^-36 of the largest
 
@@ -123,7 +125,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     pdl_wait();
     pdl_trigger();                                     // after the wait: the merge may read the lists at once
     // the barriers are visible after list_share's barriers
-    const ListShare sh = list_share<(kQ8Warps + 1) * 32>(count, g.B * g.Hkv, cta, (int)gridDim.x, kQ8Per, share_sh);
+    const ListShare sh = list_share<(kQ8Warps + 1) * 32>(count, g.B * g.Hkv, cta, (int)gridDim.x, kQ8Merge, share_sh);
     if (tid == 0 && cta == 0) offs[g.B * g.Hkv] = sh.U;   // for the merge
     if (sh.lo >= sh.hi) return;                        // whole CTA: nothing listed for it
     volatile int* abort_flag = &abort_sh;
@@ -455,7 +457,7 @@ decode_q8_combine_kernel(const int* __restrict__ count, const int* __restrict__ 
     const int bh = blockIdx.x, b = bh / g.Hq, h = bh % g.Hq, bg = b * g.Hkv + h / g.G, hl = h % g.G;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const ListPlace at = list_place<128>(count, offs, g.B * g.Hkv, bg, place_sh);
-    const ListSplit sp(at.U, nctas, kQ8Per);
+    const ListSplit sp(at.U, g.B * g.Hkv, nctas, kQ8Merge);
     int c0 = 0, np = 0;
     if (at.n > 0) {
         c0 = sp.cta_of(at.o0);

@@ -220,10 +220,12 @@ __device__ __forceinline__ float lane_start(float y, float alpha) {
     return alpha == 1.5f ? lane_start_t<1>(y, alpha) : alpha == 2.0f ? lane_start_t<2>(y, alpha) : lane_start_t<0>(y, alpha);
 }
 
-// CTAs that share U blocks: at most `grid`, and (per > 1) at least `per` blocks each where U
-// allows, so that short lists are not cut into pieces whose merge costs more than they save.
-__host__ __device__ inline int split_ctas(int U, int grid, int per) {
-    const unsigned n = ((unsigned)U + per - 1) / per;
+// CTAs that share the U entries of `lists` lists: at most `grid`, and no more than pay.  p CTAs on a list of
+// e entries take e / p entries' time, and its merge p pieces'; with an entry as long as `ratio` pieces,
+// p = sqrt(e ratio), or sqrt(e / ratio) entries a CTA.  ratio 0: pieces cost nothing to speak of.
+__device__ __forceinline__ int split_ctas(int U, int lists, int grid, int ratio) {
+    const unsigned per = ratio > 0 ? (unsigned)fmaxf(1.0f, sqrtf((float)U / ((float)lists * (float)ratio))) : 1u;
+    const unsigned n = ((unsigned)U + per - 1u) / per;
     return n < (unsigned)grid ? (int)n : grid;
 }
 
@@ -231,7 +233,8 @@ __host__ __device__ inline int split_ctas(int U, int grid, int per) {
 // (n <= kDecodeMaxCtas; a 64-bit division costs a few hundred cycles where a step has none to lose).
 struct ListSplit {
     unsigned U, n, q, r;
-    __device__ __forceinline__ ListSplit(int U_, int grid, int per) : U((unsigned)U_), n((unsigned)split_ctas(U_, grid, per)) {
+    __device__ __forceinline__ ListSplit(int U_, int lists, int grid, int ratio)
+        : U((unsigned)U_), n((unsigned)split_ctas(U_, lists, grid, ratio)) {
         q = n ? U / n : 0u;
         r = U - q * n;
     }
@@ -248,8 +251,8 @@ struct ListSplit {
 
 // CTA c's range and the number of CTAs.  Not inlined: in line, its divisions cost the attention kernels
 // registers to the end (240 bytes of spills a thread in the 8-bit tree variant).
-static __device__ __noinline__ int3 cta_range(int U, int grid, int per, int c) {
-    const ListSplit sp(U, grid, per);
+static __device__ __noinline__ int3 cta_range(int U, int lists, int grid, int ratio, int c) {
+    const ListSplit sp(U, lists, grid, ratio);
     return make_int3(sp.lo(c), sp.lo(c + 1), (int)sp.n);
 }
 
@@ -295,7 +298,7 @@ struct ListShare {
     int U, nC, lo, hi, first, o_first, o_end;
 };
 template <int NT>
-__device__ __forceinline__ ListShare list_share(const int* count, int lists, int cta, int grid, int per, int* sh) {
+__device__ __forceinline__ ListShare list_share(const int* count, int lists, int cta, int grid, int ratio, int* sh) {
     constexpr int KEEP = 4;                            // lengths a thread keeps
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int chunk = (lists + NT - 1) / NT, i0 = min(lists, tid * chunk), i1 = min(lists, i0 + chunk);
@@ -321,7 +324,7 @@ __device__ __forceinline__ ListShare list_share(const int* count, int lists, int
         if (w < warp) pre += sh[w];
         r.U += sh[w];
     }
-    const int3 range = cta_range(r.U, grid, per, cta);
+    const int3 range = cta_range(r.U, lists, grid, ratio, cta);
     r.nC = range.z;
     r.lo = r.hi = 0;
     if (cta < r.nC) {
@@ -429,7 +432,7 @@ static __device__ void decode_plan_tail(const int* count, int* offs, int* plan, 
         U += wsum[w];
     }
     if (threadIdx.x == 0) offs[BH] = U;
-    nctas = split_ctas(U, nctas, 1);                  // the attention pass uses min(grid, U) CTAs
+    nctas = min(U, nctas);                            // the attention pass uses min(grid, U) CTAs
     for (int i0 = lo; i0 < hi; i0 += 32) {
         const int i = i0 + lane;
         const int v = i < hi ? __ldcg(count + i) : 0;

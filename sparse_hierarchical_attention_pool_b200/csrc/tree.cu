@@ -326,8 +326,6 @@ tree_select_kernel(TreeArgs a, TreeWork w, TreeGeom g, float alpha, float cx) {
 
 // ------------------------------------------------------------------ host side
 
-constexpr int kTreePer = 4;          // list entries per CTA at least
-
 // one CTA per SM (its operand rings fill the shared memory)
 static int tree_ctas() {
     int dev = 0, n = 148;
@@ -350,7 +348,7 @@ static cudaError_t launch_tree_t(const TreeArgs& a, const TreeGeom& g, char* ws,
     const PdlConfig c((unsigned)g.tiles * (kTreeRows / kTreeSelWarps), kTreeSelWarps * 32, sm, stream);
     e = cudaLaunchKernelEx(&c.cfg, tree_select_kernel, a, w, g, alpha, cx);
     if (e != cudaSuccess) return e;
-    return launch_tree_attn(a, w, g, e_pow, sm2, nctas, kTreePer, stream);
+    return launch_tree_attn(a, w, g, e_pow, sm2, nctas, stream);
 }
 
 cudaError_t launch_tree(const TreeArgs& a, const TreeGeom& g, char* ws, float alpha, float coarse_scale, cudaStream_t stream) {

@@ -47,6 +47,6 @@ __device__ __forceinline__ bool tree_live(const int* kv_len, const int* n_nodes,
 
 // attention over the tiles' lists on nctas CTAs (at least `per` entries each), and the merge
 cudaError_t launch_tree_attn(const TreeArgs& a, const TreeWork& w, const TreeGeom& g, float e_pow, float sm2, int nctas,
-                             int per, cudaStream_t stream);
+                             cudaStream_t stream);
 
 }  // namespace dash

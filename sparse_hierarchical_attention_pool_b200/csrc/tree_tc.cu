@@ -7,8 +7,10 @@
 // are A operands in TMEM: with both in shared memory its 128 bytes a cycle were what bounded
 // a step (80 KB of operands and 48 KB of writes; now 32 KB and 32 KB), not HBM.
 //
-// Work split as in decode_q8.cu: the lists laid end to end hold U entries, CTA c of n takes
-// entries [U c / n, U (c + 1) / n); a tile inside one CTA is finished there, the others leave
+// Work split as in decode_q8.cu, but with as many CTAs as there are entries (an entry is 1.5 us of its CTA, a
+// piece one more of the merge's loads that go out together; 2 x 0.9K, 5 nodes: 4 entries a CTA at least
+// 26.7 us a step, 2 24.6, 1 20.6): the lists laid end to end hold U entries, CTA c of n takes entries
+// [U c / n, U (c + 1) / n); a tile inside one CTA is finished there, the others leave
 // (max, sum, output) per row in slot CTA + tile for tree_combine_kernel.
 //
 // Roles (warps): 0 - 7 softmax, two groups of 128 threads (one per row) that take the steps
@@ -78,7 +80,7 @@ template <int D, bool Q8>
 __global__ void __launch_bounds__(kTtThreads<Q8>, 1)
 tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ CUtensorMap tm_kd, const __grid_constant__ CUtensorMap tm_vd, TreeArgs a,
-                 TreeWork w, TreeGeom g, float e_pow, float sm2, int per) {
+                 TreeWork w, TreeGeom g, float e_pow, float sm2) {
     using L = TtLayout<D, Q8>;
     using namespace sm100;
     constexpr int KS = L::kKS, VS = L::kVS;
@@ -129,7 +131,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     pdl_wait();
     pdl_trigger();                                               // after the wait: the merge may read the lists at once
     // its barriers also publish the set-up above
-    const ListShare sh = list_share<NT>(w.count, g.tiles, cta, (int)gridDim.x, per, share_sh);
+    const ListShare sh = list_share<NT>(w.count, g.tiles, cta, (int)gridDim.x, 0, share_sh);
     tc_fence_after();
     if (cta == 0 && tid == 0) w.offs[g.tiles] = sh.U;
     const uint32_t tmem = tmem_sh;
@@ -691,7 +693,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 // lists' lengths, which are there before the attention ends.
 template <int D, int PG>
 __global__ void __launch_bounds__(256)
-tree_combine_kernel(TreeArgs a, TreeWork w, TreeGeom g, int nctas, int per) {
+tree_combine_kernel(TreeArgs a, TreeWork w, TreeGeom g, int nctas) {
     constexpr int RPC = 1024 / (D * PG), RW = (RPC + 7) / 8, KB = 8;   // RW: rows whose weights a warp makes
     __shared__ float wt_sh[RPC][kDecodeMaxCtas], inv_sh[RPC];
     __shared__ float4 sum_sh[PG][256 / PG];
@@ -701,7 +703,7 @@ tree_combine_kernel(TreeArgs a, TreeWork w, TreeGeom g, int nctas, int per) {
     const int bg = tile / g.tiles_bg, b = bg / g.Hkv, row0 = (tile % g.tiles_bg) * kTreeRows + r0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const ListPlace at = list_place<256>(w.count, w.offs, g.tiles, tile, place_sh);
-    const ListSplit sp(at.U, nctas, per);
+    const ListSplit sp(at.U, g.tiles, nctas, 0);
     int c0 = 0, np = 1;
     if (at.n > 0) {
         c0 = sp.cta_of(at.o0);
@@ -790,7 +792,7 @@ tree_combine_kernel(TreeArgs a, TreeWork w, TreeGeom g, int nctas, int per) {
 
 template <int D, bool Q8>
 static cudaError_t launch_t(const TreeArgs& a, const TreeWork& w, const TreeGeom& g, float e_pow, float sm2, int nctas,
-                            int per, cudaStream_t stream) {
+                            cudaStream_t stream) {
     CUtensorMap tk = {}, tv = {}, tkd = {}, tvd = {};
     if constexpr (!Q8) {
         const unsigned long long rows = (unsigned long long)g.B * g.Hkv * g.Tmax, drows = (unsigned long long)g.B * g.Hkv * g.N;
@@ -802,7 +804,7 @@ static cudaError_t launch_t(const TreeArgs& a, const TreeWork& w, const TreeGeom
     cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
     if (e != cudaSuccess) return e;
     const PdlConfig ca(nctas, kTtThreads<Q8>, sm, stream);
-    e = cudaLaunchKernelEx(&ca.cfg, tree_attn_kernel<D, Q8>, tk, tv, tkd, tvd, a, w, g, e_pow, sm2, per);
+    e = cudaLaunchKernelEx(&ca.cfg, tree_attn_kernel<D, Q8>, tk, tv, tkd, tvd, a, w, g, e_pow, sm2);
     if (e != cudaSuccess) return e;
     // few tiles: long lists of pieces and few CTAs, so four threads share a sum (one of 128 rows and 37
     // pieces a row: 14 us without); many tiles have a few pieces each
@@ -810,18 +812,18 @@ static cudaError_t launch_t(const TreeArgs& a, const TreeWork& w, const TreeGeom
     const bool wide = (long long)g.tiles * rows * D / 1024 <= nctas;
     const int rpc = 1024 / D / (wide ? 4 : 1);
     const PdlConfig cc((unsigned)g.tiles * ((rows + rpc - 1) / rpc), 256, 0, stream);
-    e = wide ? cudaLaunchKernelEx(&cc.cfg, tree_combine_kernel<D, 4>, a, w, g, nctas, per)
-             : cudaLaunchKernelEx(&cc.cfg, tree_combine_kernel<D, 1>, a, w, g, nctas, per);
+    e = wide ? cudaLaunchKernelEx(&cc.cfg, tree_combine_kernel<D, 4>, a, w, g, nctas)
+             : cudaLaunchKernelEx(&cc.cfg, tree_combine_kernel<D, 1>, a, w, g, nctas);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_tree_attn(const TreeArgs& a, const TreeWork& w, const TreeGeom& g, float e_pow, float sm2, int nctas,
-                             int per, cudaStream_t stream) {
+                             cudaStream_t stream) {
     if (nctas < 1 || nctas > kDecodeMaxCtas) return cudaErrorInvalidValue;
-    if (g.d == 128) return a.k_scale ? launch_t<128, true>(a, w, g, e_pow, sm2, nctas, per, stream)
-                                     : launch_t<128, false>(a, w, g, e_pow, sm2, nctas, per, stream);
-    return a.k_scale ? launch_t<64, true>(a, w, g, e_pow, sm2, nctas, per, stream)
-                     : launch_t<64, false>(a, w, g, e_pow, sm2, nctas, per, stream);
+    if (g.d == 128) return a.k_scale ? launch_t<128, true>(a, w, g, e_pow, sm2, nctas, stream)
+                                     : launch_t<128, false>(a, w, g, e_pow, sm2, nctas, stream);
+    return a.k_scale ? launch_t<64, true>(a, w, g, e_pow, sm2, nctas, stream)
+                     : launch_t<64, false>(a, w, g, e_pow, sm2, nctas, stream);
 }
 
 }  // namespace dash
