@@ -304,3 +304,33 @@ def test_two_trees_at_once_from_graphs_with_any_workspace(q8):
         torch.cuda.synchronize()
         for _, _, out, alone, *_ in sides:
             assert torch.equal(out.view(torch.int16), alone.view(torch.int16))
+
+
+@gpu
+def test_refusals_with_gpu_tensors_and_a_stream_argument():
+    B, Hq, Hkv, T, d, N = 2, 4, 2, 128, 64, 4
+    _, (_, k, v) = inputs.make("16k", B=B, Hq=Hq, Hkv=Hkv, T=T, d=d, n_topics=2, seed=141)
+    q, kd, vd = (x.cuda() for x in drafts(B, Hq, Hkv, N, d, 142, n_topics=2))
+    c, par, lens = filled(B, Hkv, T, d, k, v), i32([[-1, 0, 1, 0]] * B), i32([100, 64])
+    call = lambda *a, **kw: da.dash_decode_tree_q8(*a, coarse_scale=CS, **kw)  # noqa: E731
+    good = [q, kd, vd, par, *c, lens]
+    want, ws = call(*good)
+    for i, bad in ((0, q.transpose(1, 2)), (0, q.float()), (1, kd[:, :1]), (3, par.long()), (4, c[0].view(torch.uint8)),
+                   (6, c[2][:, :, :64]), (8, c[4].half()), (9, lens.cpu()), (9, lens[:1])):
+        with pytest.raises(ValueError):
+            call(*good[:i], bad, *good[i + 1:])
+    with pytest.raises(ValueError):
+        call(*good, out=torch.empty_like(q).transpose(0, 1).contiguous())
+    with pytest.raises(ValueError):
+        call(*good, workspace=ws.cpu())
+    for small in (ws[:-256], ws[16:]):                               # too small, not aligned
+        with pytest.raises(da.DashError):
+            call(*good, workspace=small)
+    with pytest.raises(da.DashError):
+        da.dash_decode_tree_q8(*good, alpha=1.0)
+    side, out = torch.cuda.Stream(), torch.full_like(want, 9.0)
+    side.wait_stream(torch.cuda.current_stream())
+    call(*good, out=out, workspace=ws, stream=side)
+    k1, _ = da.dash_cache_read(*c[:4], T, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(k1, da.dash_cache_read(*c[:4], T)[0])
