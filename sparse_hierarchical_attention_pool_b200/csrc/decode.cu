@@ -75,8 +75,12 @@ __device__ __forceinline__ void clear_header(WsHeader* hdr, bool first) {
     if (hdr && first && threadIdx.x < sizeof(WsHeader) / 16) reinterpret_cast<uint4*>(hdr)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// CTAs of two warps: at 97 registers a thread more of them fit an SM than of eight, and a short step's
+// tasks reach more SMs (8 x 96K: 13.2 us against 13.6; an 8-bit step at 16K 21.8 against 22.8).
+constexpr int kScoreThreads = 64;
+
 template <int D, int GP>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kScoreThreads)
 decode_scores_kernel(const __nv_bfloat16* __restrict__ q, const float* __restrict__ ksum,
                      const int* __restrict__ kv_len, float* __restrict__ xs, DecodeGeom g, float cx,
                      WsHeader* __restrict__ hdr) {
@@ -222,8 +226,8 @@ void launch_scores_gp(const __nv_bfloat16* q, const float* ksum, const int* kv_l
                       const DecodeGeom& g, float cx, WsHeader* hdr, cudaStream_t stream) {
     using S = ScoreShape<D, GP>;
     const long long warps = (long long)g.B * g.Hkv * ((g.nbs + S::RW - 1) / S::RW);
-    const unsigned grid = (unsigned)((warps + 7) / 8);
-    if (grid > 0) decode_scores_kernel<D, GP><<<grid, 256, 0, stream>>>(q, ksum, kv_len, xs, g, cx, hdr);
+    const unsigned grid = (unsigned)((warps + kScoreThreads / 32 - 1) / (kScoreThreads / 32));
+    if (grid > 0) decode_scores_kernel<D, GP><<<grid, kScoreThreads, 0, stream>>>(q, ksum, kv_len, xs, g, cx, hdr);
 }
 
 template <int D>
