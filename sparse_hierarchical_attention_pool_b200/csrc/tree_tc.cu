@@ -22,7 +22,7 @@
 //
 // 8-bit cache: warp 8 streams codes and scale bytes with bulk copies into a ring of their own, and
 // warps 12 - 15 (K) and 16 - 19 (V) turn them into bf16 operand tiles (exact: cache8.cuh) or load
-// the draft's bf16 rows.  Two warps a tensor convert too slowly (32K, 8 x 24 rows: 112 us a step
+// the draft's bf16 rows.  Two warps a tensor convert too slowly (32K, 4 x 24 nodes: 112 us a step
 // against 93), eight gain nothing; tiles of f16 codes with the scales outside the product save
 // conversions but need another factor per step in every role, and measured 115.
 //
