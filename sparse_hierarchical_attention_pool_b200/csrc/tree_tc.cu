@@ -558,6 +558,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
                     for (int i = 4; i < 32; ++i) m4[i & 3] = max3(m4[i & 3], __uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]));
                     if (lp2 > -INFINITY) mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), scale, lp2);
+                    // Maxima leave NaN out.  Beside a score that counts it reaches the sum by itself; where no
+                    // attended score is above -inf (a root whose own key is no number attends itself alone here)
+                    // the entry would be passed over, so the scores' sum, which is NaN or -inf, tells
+                    if (lp2 > -INFINITY && !(mx > -INFINITY)) {
+                        float all = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) all += __uint_as_float(sr[i]);
+                        if (all != all) {
+                            l_run = all;                         // NaN from here on
+                            if (m_run == -INFINITY) m_run = 0.f; // the merge takes the group's sum up
+                        }
+                    }
                 }
                 tc_fence_before();
                 arrive(bar(B_SE + grp));
@@ -629,7 +641,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 const float M = fmaxf(m0, m1);
                 const float w0 = m0 == -INFINITY ? 0.f : exp2f(m0 - M), w1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
                 const float l0 = l_sh[0][r], l1 = l_sh[1][r];
-                const float den = (w0 > 0.f ? l0 * w0 : 0.f) + (w1 > 0.f ? l1 * w1 : 0.f);
+                // a sum that is NaN counts whatever its weight is
+                const float den = (m0 == -INFINITY ? 0.f : l0 * w0) + (m1 == -INFINITY ? 0.f : l1 * w1);
                 // whether the tile lies in this CTA's range
                 const bool direct = sh.lo <= o0 && o1 <= sh.hi;
                 // partial of a tile: (max, sum) per row, then the outputs as [dims / 4][row][4], which
