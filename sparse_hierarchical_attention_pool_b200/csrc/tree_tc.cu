@@ -558,29 +558,19 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
                     for (int i = 4; i < 32; ++i) m4[i & 3] = max3(m4[i & 3], __uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]));
                     if (lp2 > -INFINITY) mx = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), scale, lp2);
-                    // Maxima leave NaN out.  Beside a score that counts it reaches the sum by itself; where no
-                    // attended score is above -inf (a root whose own key is no number attends itself alone here)
-                    // the entry would be passed over, so the scores' sum, which is NaN or -inf, tells
-                    if (lp2 > -INFINITY && !(mx > -INFINITY)) {
-                        float all = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) all += __uint_as_float(sr[i]);
-                        if (all != all) {
-                            l_run = all;                         // NaN from here on
-                            if (m_run == -INFINITY) m_run = 0.f; // the merge takes the group's sum up
-                        }
-                    }
                 }
                 tc_fence_before();
                 arrive(bar(B_SE + grp));
-                const bool active = mx > -INFINITY;
+                // Maxima leave NaN out, so an entry is not passed over by its maximum: a row may attend one key
+                // of it alone (a root its own), and where that is no number the sum has to be NaN
+                const bool active = lp2 > -INFINITY;
                 float factor = 1.f;
                 bool resc = false;
-                if (active) {
+                if (mx > -INFINITY) {
                     if (m_run == -INFINITY) m_run = mx;
                     else if (mx > m_run + kTtLazy) { factor = exp2f(m_run - mx); m_run = mx; resc = true; }
                 }
-                const float c0 = lp2 - m_run;
+                const float c0 = m_run == -INFINITY ? lp2 : lp2 - m_run;
                 const uint64_t sc2 = f2_pack(__float_as_uint(scale), __float_as_uint(scale));
                 const uint64_t c2 = f2_pack(__float_as_uint(c0), __float_as_uint(c0));
                 uint32_t pk[32];
@@ -625,6 +615,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 arrive(bar(B_PF + grp));
             }
             if (tid == 0 && e0 == 0) w.offs[tile] = o0;          // for the merge of a split tile
+            if (l_run != l_run && m_run == -INFINITY) m_run = 0.f;   // no score but NaN: the merge takes the sum up
             // ---- the two groups' states: (max, sum, output) of every row
             m_sh[grp][r] = m_run;
             l_sh[grp][r] = l_run;
