@@ -491,7 +491,9 @@ cudaError_t launch_decode_lists(const void* q, const float* ksum, const int* kv_
     const char* init = getenv("DASH_ENTMAX_INIT");
     const int hist_init = (init && strcmp(init, "histogram") == 0) ? 1 : 0;
     const int sm = (gl.nbs < kSelCap ? gl.nbs : kSelCap) * (kSelThreads / 32) * (int)sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(decode_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+    // the attribute is the function's, not the call's: another host thread's shorter cache must not lower it
+    cudaError_t e = cudaFuncSetAttribute(decode_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSelCap * (kSelThreads / 32) * (int)sizeof(float));
     if (e != cudaSuccess) return e;
     PdlConfig c(gl.B * gl.Hkv, kSelThreads, sm, stream);
     if (!pdl) c.cfg.numAttrs = 0;

@@ -343,7 +343,9 @@ static cudaError_t launch_tree_t(const TreeArgs& a, const TreeGeom& g, char* ws,
     const int nctas = tree_ctas();
     tree_scores_kernel<D, Q8><<<gs, 128, 0, stream>>>(a, w, g, cx);
     const int sm = (g.cap < kSelCap ? g.cap : kSelCap) * kTreeSelWarps * (int)sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(tree_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+    // the attribute is the function's, not the call's: another host thread's shorter cache must not lower it
+    cudaError_t e = cudaFuncSetAttribute(tree_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSelCap * kTreeSelWarps * (int)sizeof(float));
     if (e != cudaSuccess) return e;
     const PdlConfig c((unsigned)g.tiles * (kTreeRows / kTreeSelWarps), kTreeSelWarps * 32, sm, stream);
     e = cudaLaunchKernelEx(&c.cfg, tree_select_kernel, a, w, g, alpha, cx);
