@@ -539,11 +539,15 @@ cudaError_t launch_decode(const void* q, const void* kc, const void* vc, const f
     }
     // the CUDA-core path has per-head priors only and no parity dump
     if (agg || x_dump) return cudaErrorNotSupported;
-    const size_t sm_attn = (size_t)4 * kBlock * g.d * sizeof(__nv_bfloat16)
-                         + (size_t)(2 * g.G * g.d + g.G * kBlock + 4 * 32) * sizeof(float);
+    auto attn_bytes = [&](int G) {
+        return (size_t)4 * kBlock * g.d * sizeof(__nv_bfloat16) + (size_t)(2 * G * g.d + G * kBlock + 4 * 32) * sizeof(float);
+    };
+    const size_t sm_attn = attn_bytes(g.G);
+    // the attribute is the function's: always the size for the most heads, so no other thread's call lowers it
+    const int sm_max = (int)attn_bytes(32);
     e = g.d == 128
-        ? cudaFuncSetAttribute(decode_attn_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm_attn)
-        : cudaFuncSetAttribute(decode_attn_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm_attn);
+        ? cudaFuncSetAttribute(decode_attn_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm_max)
+        : cudaFuncSetAttribute(decode_attn_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm_max);
     if (e != cudaSuccess) return e;
     dim3 ga(BH, g.maxchunks);
     if (g.d == 128)

@@ -82,3 +82,10 @@ def race(calls, steps=4000):
 def test_threads_with_caches_of_different_lengths(op):
     """Four threads a length: what a step asks of a kernel's shared memory follows from the cache's length."""
     race([make(op, T, 2, 1, 64, i) for i, T in enumerate((64, 4096) * 4)])
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_threads_with_different_numbers_of_heads(d):
+    """More than 8 heads per KV head: the attention's shared memory grows with their number."""
+    race([make("decode", 128, Hq, 1, d, i) for i, Hq in enumerate((9, 32) * 4)])
