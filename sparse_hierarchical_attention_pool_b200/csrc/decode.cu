@@ -261,7 +261,7 @@ decode_select_kernel(const int* __restrict__ kv_len, const float* __restrict__ x
     __shared__ HistBins hist[kSelThreads / 32];
     __shared__ unsigned bitmap[kWords];
     __shared__ int list_sh[33 * (kSelThreads / 32)];
-    extern __shared__ float rows_sm[];
+    extern __shared__ __align__(16) float rows_sm[];   // rows in 16-byte chunks
     const int scap = min(g.nbs, kSelCap);
     const int bg = blockIdx.x, b = bg / g.Hkv, kvh = bg % g.Hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = kSelThreads / 32;

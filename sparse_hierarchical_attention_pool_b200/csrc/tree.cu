@@ -243,7 +243,7 @@ constexpr int kTreeSelWarps = 8;
 __global__ void __launch_bounds__(kTreeSelWarps * 32)
 tree_select_kernel(TreeArgs a, TreeWork w, TreeGeom g, float alpha, float cx) {
     __shared__ int last_sh, list_sh[33 * kTreeSelWarps];
-    extern __shared__ float rows_sm[];
+    extern __shared__ __align__(16) float rows_sm[];   // rows in 16-byte chunks
     const int scap = min(g.cap, kSelCap);
     constexpr int kCtasPerTile = kTreeRows / kTreeSelWarps;
     const int tile = blockIdx.x / kCtasPerTile, sub = blockIdx.x % kCtasPerTile;
