@@ -246,9 +246,9 @@ void launch_scores(const __nv_bfloat16* q, const float* ksum, const int* kv_len,
 // ------------------------------------------------------------------ select
 
 // One CTA of 8 warps per (b, kv head).  Warp w solves the thresholds of heads w, w + 8, ...
-// with the row in shared memory (one warp per head: no cross-warp reduction in a pass).  The
-// heads' selected blocks are OR-ed into a bitmap, which becomes the group's list, the own block
-// last.
+// with the row in shared memory, scap values of it at most (one warp per head: no cross-warp
+// reduction in a pass).  The heads' selected blocks are OR-ed into a bitmap, which becomes the
+// group's list, the own block last.
 constexpr int kSelThreads = 256;
 
 __global__ void __launch_bounds__(kSelThreads)
@@ -256,13 +256,12 @@ decode_select_kernel(const int* __restrict__ kv_len, const float* __restrict__ x
                      float* __restrict__ tau, int* __restrict__ list, int* __restrict__ count,
                      int* __restrict__ done, int* __restrict__ offs, int* __restrict__ plan,
                      __nv_bfloat16* __restrict__ out, WsHeader* __restrict__ hdr, DecodeGeom g,
-                     float alpha, int nctas, int hist_init, bool warm) {
+                     float alpha, int nctas, int hist_init, bool warm, int scap) {
     constexpr int kWords = kMaxT / kBlock / 32;
     __shared__ HistBins hist[kSelThreads / 32];
     __shared__ unsigned bitmap[kWords];
     __shared__ int list_sh[33 * (kSelThreads / 32)];
     extern __shared__ __align__(16) float rows_sm[];   // rows in 16-byte chunks
-    const int scap = min(g.nbs, kSelCap);
     const int bg = blockIdx.x, b = bg / g.Hkv, kvh = bg % g.Hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = kSelThreads / 32;
     const int cap = g.nbs + 1;
@@ -490,10 +489,12 @@ cudaError_t launch_decode_lists(const void* q, const float* ksum, const int* kv_
     // costs more than the passes it saves)
     const char* init = getenv("DASH_ENTMAX_INIT");
     const int hist_init = (init && strcmp(init, "histogram") == 0) ? 1 : 0;
-    const int sm = (gl.nbs < kSelCap ? gl.nbs : kSelCap) * (kSelThreads / 32) * (int)sizeof(float);
+    const int rows = gl.G < kSelThreads / 32 ? gl.G : kSelThreads / 32;            // rows that a CTA holds at a time
+    const int fit = kSelBytes / (rows * (int)sizeof(float)) & ~31;
+    const int scap = gl.nbs < fit ? gl.nbs : fit;
+    const int sm = scap * rows * (int)sizeof(float);
     // the attribute is the function's, not the call's: another host thread's shorter cache must not lower it
-    cudaError_t e = cudaFuncSetAttribute(decode_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSelCap * (kSelThreads / 32) * (int)sizeof(float));
+    cudaError_t e = cudaFuncSetAttribute(decode_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelBytes);
     if (e != cudaSuccess) return e;
     PdlConfig c(gl.B * gl.Hkv, kSelThreads, sm, stream);
     if (!pdl) c.cfg.numAttrs = 0;
@@ -501,7 +502,7 @@ cudaError_t launch_decode_lists(const void* q, const float* ksum, const int* kv_
                            reinterpret_cast<int*>(ws + gl.off_list), reinterpret_cast<int*>(ws + gl.off_count),
                            reinterpret_cast<int*>(ws + gl.off_done), reinterpret_cast<int*>(ws + gl.off_offs),
                            reinterpret_cast<int*>(ws + gl.off_plan), static_cast<__nv_bfloat16*>(out), hdr, gl, alpha, nctas,
-                           hist_init, pdl);
+                           hist_init, pdl, scap);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

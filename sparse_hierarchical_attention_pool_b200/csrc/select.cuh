@@ -7,13 +7,21 @@
 
 namespace dash {
 
-// Row values a warp keeps in shared memory at most (128 KB for a CTA of 8 warps; shorter rows take
-// less).  With 1536 a step at 262,144 tokens reads the rest from memory in every pass: a tree of 16
+// Shared memory of a decode step's select CTA for the rows it holds at a time (up to 8, one per warp): as many
+// values of each as fit, and the rest from memory in every pass.  It is shared out over the rows there are: one
+// head a group at 262,144 tokens needs 16 KB, not room for 8 rows, and several CTAs fit an SM (40 sequences of 8
+// groups: 593 us a step against 655).  This is what an SM has beside the kernel's own 13 KB; at 1,048,576
+// tokens, 4 heads, 4 sequences of 2 groups, a step takes 421 us with 24 KB, 364 with 96, 336 with 128 and 272
+// with this (237 with passes over eight values at a time in place of four).
+constexpr int kSelBytes = 208 * 1024;
+
+// Row values a warp of a tree step's select CTA keeps in shared memory at most (128 KB for its 8 rows; shorter
+// rows take less).  With 1536 a step at 262,144 tokens reads the rest from memory in every pass: a tree of 16
 // over 2 KV heads takes 172 us, and 115 with 4096.
 constexpr int kSelCap = 4096;
 
 // Row values of one row on one warp, in shared memory: lane l holds x[l + 32 k]; values past the
-// buffer are read from memory. 
+// buffer are read from memory.  The buffer holds a multiple of 32 values, or the whole row.
 struct WarpRow {
     const float *s, *p;
     int lane, n, ns;
@@ -33,7 +41,7 @@ struct WarpRow {
     template <class F>
     __device__ __forceinline__ void each(F&& f) const {
         int j = lane;
-#pragma unroll 4
+#pragma unroll 8
         for (; j < ns; j += 32) f(j, s[j]);
 #pragma unroll 8
         for (; j < n; j += 32) f(j, p[j]);
@@ -54,14 +62,23 @@ struct WarpRow {
         for (int k0 = 0; k0 * 32 < n; k0 += 32) {
             const int kn = min(32, (n - k0 * 32 + 31) / 32);
             unsigned mine = 0u;
+            const int ks = max(0, min(kn, (ns + 31) / 32 - k0));         // words whose values are in the buffer
 #pragma unroll 8
-            for (int k = 0; k < kn; ++k) {
+            for (int k = 0; k < ks; ++k) {
                 const int j = (k0 + k) * 32 + lane;
-                float v = -INFINITY;
-                if (j < ns) v = s[j];
-                else if (j < n) v = p[j];
-                const unsigned w = __ballot_sync(0xffffffffu, v > t);
+                const unsigned w = __ballot_sync(0xffffffffu, (j < ns ? s[j] : -INFINITY) > t);
                 mine = lane == k ? w : mine;
+            }
+            // the others eight at a time: a load behind each ballot would wait for memory once a word
+            for (int k = ks; k < kn; k += 8) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = p[min((k0 + k + i) * 32 + lane, n - 1)];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const unsigned w = __ballot_sync(0xffffffffu, (k0 + k + i) * 32 + lane < n && v[i] > t);
+                    mine = lane == k + i ? w : mine;                     // 0 from word kn on
+                }
             }
             bits += __popc(mine);
             if (mine) f(k0 + lane, mine);
