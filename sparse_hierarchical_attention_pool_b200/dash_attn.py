@@ -9,6 +9,7 @@ Tensor conventions follow the header: bf16, contiguous, q/out [B, Hq, T, d], k/v
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -528,6 +529,16 @@ def _ksum(ksum, B, Hkv, Tmax, d, block, dev):
     return _ptr(ksum, torch.float32, (B, Hkv, n if n or ksum.shape[2] == 0 else 1, d), dev, "ksum")
 
 
+def _on(stream, dev):
+    """Context in which a call's own tensors are allocated: with a stream given they belong to it, so their
+    memory is neither taken from work that is pending on the current stream nor given back to it early."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if stream.device.index != dev:
+        raise ValueError(f"stream is on device {stream.device.index}, the call's first tensor on {dev}")
+    return torch.cuda.stream(stream)
+
+
 def _run(name, dev, stream, *args):
     """Call a library function with the tensors' device current, on `stream` or that device's
     current stream."""
@@ -589,12 +600,13 @@ def dash_cache_read(k_cache, v_cache, k_scale, v_scale, n, start=None, kv_len=No
     behind kv_len[b] are zero.  start, kv_len int32 [B] (None: 0 and Tmax)."""
     B, Hkv, Tmax, d = k_cache.shape
     dev, full, flat, rows = k_cache.get_device(), (B, Hkv, Tmax, d), (B, Hkv, Tmax), (B, Hkv, n, d)
-    if k_out is None and v_out is None:
-        k_out, v_out = torch.empty((2, *rows), dtype=torch.bfloat16, device=k_cache.device).unbind()
-    elif k_out is None:
-        k_out = torch.empty(rows, dtype=torch.bfloat16, device=k_cache.device)
-    elif v_out is None:
-        v_out = torch.empty(rows, dtype=torch.bfloat16, device=k_cache.device)
+    with _on(stream, dev):
+        if k_out is None and v_out is None:
+            k_out, v_out = torch.empty((2, *rows), dtype=torch.bfloat16, device=k_cache.device).unbind()
+        elif k_out is None:
+            k_out = torch.empty(rows, dtype=torch.bfloat16, device=k_cache.device)
+        elif v_out is None:
+            v_out = torch.empty(rows, dtype=torch.bfloat16, device=k_cache.device)
     args = (_ptr(k_cache, _E4M3, full, dev, "k_cache"), _ptr(v_cache, _E4M3, full, dev, "v_cache"),
             _ptr(k_scale, _U8, flat, dev, "k_scale"), _ptr(v_scale, _U8, flat, dev, "v_scale"),
             _opt(start, torch.int32, (B,), dev, "start"), _opt(kv_len, torch.int32, (B,), dev, "kv_len"),
@@ -625,13 +637,15 @@ def dash_decode_q8(q, k_cache, v_cache, k_scale, v_scale, ksum, kv_len, out=None
     Hkv, Tmax = k_cache.shape[1], k_cache.shape[2]
     dev, full, flat = q.get_device(), (B, Hkv, Tmax, d), (B, Hkv, Tmax)
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream, dev):
+            out = torch.empty_like(q)
     args = (_ptr(q, torch.bfloat16, q.shape, dev, "q"),
             _ptr(k_cache, _E4M3, full, dev, "k_cache"), _ptr(v_cache, _E4M3, full, dev, "v_cache"),
             _ptr(k_scale, _U8, flat, dev, "k_scale"), _ptr(v_scale, _U8, flat, dev, "v_scale"),
             _ksum(ksum, B, Hkv, Tmax, d, block, dev), _ptr(kv_len, torch.int32, (B,), dev, "kv_len"),
             _ptr(out, torch.bfloat16, q.shape, dev, "out"))
-    workspace = _space(workspace, decode_q8_workspace_size, (B, Hq, Hkv, Tmax, d, block), q.device)
+    with _on(stream, dev):
+        workspace = _space(workspace, decode_q8_workspace_size, (B, Hq, Hkv, Tmax, d, block), q.device)
     _run("dash_decode_q8", dev, stream, *args, B, Hq, Hkv, Tmax, d, block, alpha, coarse_scale,
          workspace.data_ptr(), workspace.numel())
     return out, workspace
@@ -643,7 +657,8 @@ def _tree(name, q, k_draft, v_draft, parent, k_cache, v_cache, scales, ksum, kv_
     Hkv, Tmax = k_cache.shape[1], k_cache.shape[2]
     dev, full, flat, draft = q.get_device(), (B, Hkv, Tmax, d), (B, Hkv, Tmax), (B, Hkv, N, d)
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream, dev):
+            out = torch.empty_like(q)
     kind = _E4M3 if scales else torch.bfloat16
     args = (_ptr(q, torch.bfloat16, q.shape, dev, "q"),
             _ptr(k_draft, torch.bfloat16, draft, dev, "k_draft"), _ptr(v_draft, torch.bfloat16, draft, dev, "v_draft"),
@@ -652,7 +667,8 @@ def _tree(name, q, k_draft, v_draft, parent, k_cache, v_cache, scales, ksum, kv_
             *[_ptr(t, _U8, flat, dev, "k_scale / v_scale") for t in scales],
             _ksum(ksum, B, Hkv, Tmax, d, block, dev), _ptr(kv_len, torch.int32, (B,), dev, "kv_len"),
             _ptr(out, torch.bfloat16, q.shape, dev, "out"))
-    workspace = _space(workspace, decode_tree_workspace_size, (B, Hq, Hkv, N, Tmax, d, block), q.device)
+    with _on(stream, dev):
+        workspace = _space(workspace, decode_tree_workspace_size, (B, Hq, Hkv, N, Tmax, d, block), q.device)
     _run(name, dev, stream, *args, B, Hq, Hkv, N, Tmax, d, block, alpha, coarse_scale,
          workspace.data_ptr(), workspace.numel())
     return out, workspace
