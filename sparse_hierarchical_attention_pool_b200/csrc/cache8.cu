@@ -135,8 +135,9 @@ cache_append_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16
             sk = old_scale;
         }
         if (want) {
-            // code * 2^(s - 127) is exact, so one fused operation adds what the cache holds
-            const float sc = scale_value(sk);
+            // code * 2^(s - 127) is exact, so one fused operation adds what the cache holds; a 64th of it, which is
+            // exact too (2^-133 at least), so that keys near the largest held number do not add up to infinity
+            const float sc = scale_value(sk) * (1.0f / kBlock);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float f[8];
@@ -159,7 +160,7 @@ cache_append_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < 8 * RPS; ++w) sum += red[w][tid];
-        ksum[((size_t)bg * (Tmax / kBlock) + j) * D + tid] = sum * (1.0f / kBlock);
+        ksum[((size_t)bg * (Tmax / kBlock) + j) * D + tid] = sum;
     }
 }
 
