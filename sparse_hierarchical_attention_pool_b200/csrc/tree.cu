@@ -94,7 +94,7 @@ __device__ __forceinline__ void tree_score_chunk(const __nv_bfloat16* q, const f
 }
 
 // Row y = 0 of the grid prepares a KV group: ancestor sets, depths, the tiles' empty bitmaps and,
-// where some path completes the open block, the sum of the open block's keys on every path.
+// where some path completes the open block, the mean of the open block's keys on every path.
 template <int D, bool Q8>
 __global__ void __launch_bounds__(128)
 tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
@@ -153,6 +153,7 @@ tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
     if (!__syncthreads_or(may_cross && r + dp >= kBlock)) return;
     const int c = tid % TPR * 4, r0 = tid / TPR;
     float t[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr float kPart = 1.0f / kBlock;                          // exact: large keys must not add up to infinity
     const size_t row0 = (size_t)bg * g.Tmax + (L - r);
 #pragma unroll 16
     for (int i = r0; i < r; i += NR) {
@@ -167,11 +168,11 @@ tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
             f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) t[k] += f[k];
+        for (int k = 0; k < 4; ++k) t[k] = fmaf(f[k], kPart, t[k]);
     }
-    // A path's sum: the cached keys of the open block and the path's tokens in it, those with
-    // r + depth < 64 (the first 64 - r of a path, so they are bits of its ancestor set).  All sums
-    // at once are one product of the 0 / 1 ancestor matrix and the keys (exact products, fp32 sums): a
+    // A path's mean: the cached keys of the open block and the path's tokens in it, those with
+    // r + depth < 64 (the first 64 - r of a path, so they are bits of its ancestor set).  All of them
+    // at once are one product of the 0 / 2^-6 ancestor matrix and the keys (exact products, fp32 sums): a
     // warp takes 16 nodes, in place of a walk of up to 64 dependent additions (4 us, now 1).
     const unsigned in_w = __ballot_sync(0xffffffffu, dp >= 0 && r + dp < kBlock);
     if (tid < kMaxNodes && (tid & 31) == 0) in_s[tid >> 5] = in_w;
@@ -198,8 +199,8 @@ tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
         for (int k = 0; k < 4; ++k) acc[n][k] = 0.f;
     unsigned odd = 0u;                                              // a key that is no number
     for (int k0 = 0; k0 < nodes; k0 += 16) {
-        // two bits as two bf16: 1 or 0
-        auto pair = [&](unsigned long long bits, int k) { return ((unsigned)(bits >> k) & 1u) * 0x3f80u | ((unsigned)(bits >> (k + 1)) & 1u) * 0x3f800000u; };
+        // two bits as two bf16: 2^-6 or 0
+        auto pair = [&](unsigned long long bits, int k) { return ((unsigned)(bits >> k) & 1u) * 0x3c80u | ((unsigned)(bits >> (k + 1)) & 1u) * 0x3c800000u; };
         const int k = k0 + 2 * t4;
         const uint32_t af[4] = {pair(a0, k), pair(a1, k), pair(a0, k + 8), pair(a1, k + 8)};
 #pragma unroll
@@ -218,7 +219,7 @@ tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
         for (int i = warp * 16; i < min(nodes, warp * 16 + 16); ++i)
             for (int e = lane; e < D; e += 32) {
                 float v = tot_s[e];
-                for (unsigned long long up = sum_s[i]; up; up &= up - 1) v += __bfloat162float(key_s[__ffsll((long long)up) - 1][e]);
+                for (unsigned long long up = sum_s[i]; up; up &= up - 1) v = fmaf(__bfloat162float(key_s[__ffsll((long long)up) - 1][e]), kPart, v);
                 dst[(size_t)i * D + e] = v;
             }
         return;
@@ -276,7 +277,7 @@ tree_select_kernel(TreeArgs a, TreeWork w, TreeGeom g, float alpha, float cx) {
                 const float* pr = w.path + ((size_t)bg * g.N + node) * g.d;
                 float s = 0.f;
                 for (int c = lane; c < g.d; c += 32) s = fmaf(__bfloat162float(qr[c]), pr[c], s);
-                s = warp_sum(s) * (cx / kBlock);
+                s = warp_sum(s) * cx;
                 // a path with a key that is no number has no such score: NaN, which makes the row NaN in the
                 // attention, and no part of the threshold (it has no root then)
                 if (!(fabsf(s) < INFINITY)) { s = __int_as_float(0x7fc00000); n = F; }

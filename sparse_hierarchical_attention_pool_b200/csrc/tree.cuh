@@ -14,7 +14,7 @@ struct TreeWork {
     float *xs, *tau;                     // scores [rows][cap], thresholds
     unsigned long long* anc;             // [B][N] ancestors and self (0: an invalid node)
     int* depth;                          // [B][N]
-    float* path;                         // [B Hkv][N][D] sum of the open block's keys on a node's path
+    float* path;                         // [B Hkv][N][D] 1 / 64 of the open block's keys on a node's path, added up
     unsigned* bits;                      // [tile][nbw] selected blocks
     int *tick, *list, *count;
     int* offs;                           // [tile] first entry of split tiles; [tiles]: entries in all

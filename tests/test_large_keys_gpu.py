@@ -1,10 +1,12 @@
-"""Keys near the largest number that the 8-bit cache holds: the summaries are their means, which are numbers
-although the keys' sum is not one in fp32."""
+"""Keys near the largest number that the 8-bit cache holds: the summaries of blocks, and of blocks that a
+drafted path completes, are their means, which are numbers although the keys' sum is not one in fp32."""
 import pytest
 import torch
 
 from sparse_hierarchical_attention_pool_b200 import dash_attn as da
-from test_cache8_gpu import i32, junk_cache
+from sparse_hierarchical_attention_pool_b200 import inputs
+from test_cache8_gpu import close, i32, junk_cache
+from test_tree_gpu import drafts, expected, run
 
 gpu = pytest.mark.gpu
 
@@ -49,3 +51,23 @@ def test_summaries_of_small_keys(p):
     # half the least subnormal fp32 where a mean is that small
     tol = 2.0 ** -18 * held.abs().mean(2) + 2.0 ** -150
     assert bool(((c[4][:, :, 0].double().cpu() - held.mean(2)).abs() <= tol).all())
+
+
+@gpu
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("where", ["cache", "draft", "both"])
+def test_paths_that_complete_a_block_of_large_keys(q8, where):
+    """The open block's keys hold bf16's largest numbers in a dim that no query has: scores and outputs are
+    those of the other dims."""
+    B, Hq, Hkv, T, d, N, dim = 1, 4, 2, 192, 64, 8, 11
+    L, parent = 128 + 59, [-1, 0, 1, 2, 3, 4, 5, 5]
+    _, (_, k, v) = inputs.make("16k", B=B, Hq=Hq, Hkv=Hkv, T=T, d=d, n_topics=2, seed=91)
+    q, kd, vd = drafts(B, Hq, Hkv, N, d, 92, n_topics=2)
+    q[..., dim] = 0.0
+    if where != "draft":
+        k[:, :, 128:140, dim] = 240.0 * 2.0 ** 120
+    if where != "cache":
+        kd[:, :, 1:4, dim] = 240.0 * 2.0 ** 120
+    got, kh, vh = run(q8, q, kd, vd, [parent], k, v, [L], 1.5, junk=False)
+    ref = expected(q[0], kd[0], vd[0], parent, kh[0], vh[0], L, 1.5)
+    close(got[0].float().cpu(), ref, float(max(vh.float().abs().max(), vd.float().abs().max())), 1.5, 8, where)
