@@ -252,7 +252,7 @@ void launch_scores(const __nv_bfloat16* q, const float* ksum, const int* kv_len,
 constexpr int kSelThreads = 256;
 
 __global__ void __launch_bounds__(kSelThreads)
-decode_select_kernel(const int* __restrict__ kv_len, const float* __restrict__ xs,
+decode_select_kernel(const __nv_bfloat16* __restrict__ q, const int* __restrict__ kv_len, const float* __restrict__ xs,
                      float* __restrict__ tau, int* __restrict__ list, int* __restrict__ count,
                      int* __restrict__ done, int* __restrict__ offs, int* __restrict__ plan,
                      __nv_bfloat16* __restrict__ out, WsHeader* __restrict__ hdr, DecodeGeom g,
@@ -288,7 +288,10 @@ decode_select_kernel(const int* __restrict__ kv_len, const float* __restrict__ x
         xr.load(xs + row * cap, rows_sm + (size_t)warp * scap, scap, lane, bt);
         float t = __int_as_float(0x7fc00000);
         const float y = xr.lane_max(), m = warp_max(y);
-        if (bt > 0) t = row_tau(xr, m, alpha, &no_conv, hist_init ? &hist[warp] : nullptr, g.maxit, warm ? lane_start(y - m, alpha) : -1.0f);
+        // warm, the 8-bit step: a head whose query is no number has nothing to solve and selects nothing (dash_decode
+        // reports such a step as not converged)
+        if (bt > 0 && !(warm && !(fabsf(m) < INFINITY) && row_not_finite(q + row * g.d, g.d)))
+            t = row_tau(xr, m, alpha, &no_conv, hist_init ? &hist[warp] : nullptr, g.maxit, warm ? lane_start(y - m, alpha) : -1.0f);
         if (lane == 0) tau[row] = t;
         const int nsel = xr.words(t, [&](int k, unsigned w) { atomicOr(&bitmap[k], w); });
         if (lane == 0) {
@@ -498,7 +501,7 @@ cudaError_t launch_decode_lists(const void* q, const float* ksum, const int* kv_
     if (e != cudaSuccess) return e;
     PdlConfig c(gl.B * gl.Hkv, kSelThreads, sm, stream);
     if (!pdl) c.cfg.numAttrs = 0;
-    e = cudaLaunchKernelEx(&c.cfg, decode_select_kernel, kv_len, (const float*)xs, reinterpret_cast<float*>(ws + gl.off_tau),
+    e = cudaLaunchKernelEx(&c.cfg, decode_select_kernel, qb, kv_len, (const float*)xs, reinterpret_cast<float*>(ws + gl.off_tau),
                            reinterpret_cast<int*>(ws + gl.off_list), reinterpret_cast<int*>(ws + gl.off_count),
                            reinterpret_cast<int*>(ws + gl.off_done), reinterpret_cast<int*>(ws + gl.off_offs),
                            reinterpret_cast<int*>(ws + gl.off_plan), static_cast<__nv_bfloat16*>(out), hdr, gl, alpha, nctas,

@@ -206,6 +206,14 @@ __device__ __forceinline__ float warp_row_tau(const WarpRow& xr, float m, float 
     return t;
 }
 
+// Whether a query holds an element that is no finite number (one warp, every lane returns it).  Its row is NaN by
+// its logits; a score of such a row that is infinite, or none that is a number, is no failed solve.
+__device__ __forceinline__ bool row_not_finite(const __nv_bfloat16* q, int d) {
+    bool bad = false;
+    for (int c = threadIdx.x & 31; c < d; c += 32) bad |= !(fabsf(__bfloat162float(q[c])) < INFINITY);
+    return __any_sync(0xffffffffu, bad);
+}
+
 // The threshold of a row whatever alpha is; m = its largest value, finite.
 __device__ __forceinline__ float row_tau(const WarpRow& xr, float m, float alpha, int* no_conv, HistBins* bins,
                                          int cap, float u0 = -1.0f) {

@@ -288,7 +288,8 @@ tree_select_kernel(TreeArgs a, TreeWork w, TreeGeom g, float alpha, float cx) {
             WarpRow xr;
             xr.load(xrow, rows_sm + (size_t)warp * scap, scap, lane, n);
             const float y = xr.lane_max(), m = warp_max(y);
-            if (m > -INFINITY) t = row_tau(xr, m, alpha, &no_conv, nullptr, g.maxit, lane_start(y - m, alpha));
+            if (m > -INFINITY && !(m == INFINITY && row_not_finite(static_cast<const __nv_bfloat16*>(a.q) + row * g.d, g.d)))
+                t = row_tau(xr, m, alpha, &no_conv, nullptr, g.maxit, lane_start(y - m, alpha));
             nsel = xr.words(t, [&](int k, unsigned sel) { atomicOr(&w.bits[(size_t)tile * g.nbw + k], sel); });
             if (lane == 0) {
                 if (no_conv) atomicOr(&w.hdr->status, kStNoConverge);
