@@ -585,13 +585,14 @@ def dash_cache_append(k_new, v_new, kv_len, k_cache, v_cache, k_scale, v_scale, 
     if n is None:
         n = rows if src is None else src.shape[1]
     dev, full, flat = k_new.get_device(), (B, Hkv, Tmax, d), (B, Hkv, Tmax)
-    _run("dash_cache_append", dev, stream,
-         _ptr(k_new, torch.bfloat16, k_new.shape, dev, "k_new"), _ptr(v_new, torch.bfloat16, k_new.shape, dev, "v_new"),
-         _opt(src, torch.int32, (B, n), dev, "src"), _opt(n_new, torch.int32, (B,), dev, "n_new"),
-         _ptr(kv_len, torch.int32, (B,), dev, "kv_len"),
-         _ptr(k_cache, _E4M3, full, dev, "k_cache"), _ptr(v_cache, _E4M3, full, dev, "v_cache"),
-         _ptr(k_scale, _U8, flat, dev, "k_scale"), _ptr(v_scale, _U8, flat, dev, "v_scale"),
-         None if ksum is None else _ksum(ksum, B, Hkv, Tmax, d, block, dev), B, Hkv, rows, n, Tmax, d, block)
+    args = (_ptr(k_new, torch.bfloat16, k_new.shape, dev, "k_new"), _ptr(v_new, torch.bfloat16, k_new.shape, dev, "v_new"),
+            _opt(src, torch.int32, (B, n), dev, "src"), _opt(n_new, torch.int32, (B,), dev, "n_new"),
+            _ptr(kv_len, torch.int32, (B,), dev, "kv_len"),
+            _ptr(k_cache, _E4M3, full, dev, "k_cache"), _ptr(v_cache, _E4M3, full, dev, "v_cache"),
+            _ptr(k_scale, _U8, flat, dev, "k_scale"), _ptr(v_scale, _U8, flat, dev, "v_scale"),
+            None if ksum is None else _ksum(ksum, B, Hkv, Tmax, d, block, dev))
+    if n != 0:                                     # no tokens: tensors without elements have no address
+        _run("dash_cache_append", dev, stream, *args, B, Hkv, rows, n, Tmax, d, block)
 
 
 def dash_cache_read(k_cache, v_cache, k_scale, v_scale, n, start=None, kv_len=None, k_out=None, v_out=None,
