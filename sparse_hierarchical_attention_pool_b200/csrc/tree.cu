@@ -150,7 +150,10 @@ tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
         }
     }
     if (tid < g.N && bg % g.Hkv == 0) { w.anc[(size_t)b * g.N + tid] = m; w.depth[(size_t)b * g.N + tid] = dp; }
-    if (!__syncthreads_or(may_cross && r + dp >= kBlock)) return;
+    if (!__syncthreads_or(may_cross && r + dp >= kBlock)) {
+        cp_async_wait<0>();                                         // the copies land before the CTA's memory is another's
+        return;
+    }
     const int c = tid % TPR * 4, r0 = tid / TPR;
     float t[4] = {0.f, 0.f, 0.f, 0.f};
     constexpr float kPart = 1.0f / kBlock;                          // exact: large keys must not add up to infinity
