@@ -192,8 +192,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
             pos = o0 + e_end;
         }
-        if (!ok && lane == 0) {
-            // let the copies already issued land before the CTA exits
+        if (lane == 0) {
+            // the copies land before the CTA exits, also where a consumer gives up after the last was issued
             volatile int dummy = 0;
             for (int s = 0; s < kQ8Stages; ++s) {
                 if (cnt <= s) continue;

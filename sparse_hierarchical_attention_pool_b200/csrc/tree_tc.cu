@@ -205,8 +205,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 ++armed;
             }
         });
-        if (!ok && lane == 0) {
-            // every load this thread started lands before the CTA exits
+        if (lane == 0) {
+            // every load this thread started lands before the CTA exits, also where another role gives up after the last
             constexpr int NS = Q8 ? kTtRaw : KS;
             volatile int dummy = 0;
             for (int st = 0; st < NS; ++st) {
@@ -262,14 +262,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(B_VF + st));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < VS; ++i)
-                            if (i == st) last_st[i] = gs + s;
                     }
+                    // the stage's last use, special entries too: an older one's parity would wait in vain
+#pragma unroll
+                    for (int i = 0; i < VS; ++i)
+                        if (i == st) last_st[i] = gs + s;
                 }
             });
-            if (!ok && lane == 0) {
+            if (lane == 0) {
                 volatile int dummy = 0;
 #pragma unroll
                 for (int i = 0; i < VS; ++i)
