@@ -93,6 +93,14 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
     return v;
 }
+// a * b, at most the largest finite number (NaN stays NaN): the factors of a key and of a query may overflow
+// together where their codes' product is zero, and the logit is zero then
+__device__ __forceinline__ float mul_finite(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, 0f7F7FFFFF;" : "=f"(r) : "f"(a * b));
+    return r;
+}
+
 template <int D>
 __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 2)
 decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -359,7 +367,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     for (int c = 0; c < 2; ++c) {
                         const float p = c ? lp.y : lp.x;
                         const bool none = off || p == -INFINITY;
-                        const float l2 = none ? -INFINITY : fmaf(s[mt][2 * hh + c], kf * qf[c], p);
+                        const float l2 = none ? -INFINITY : fmaf(s[mt][2 * hh + c], mul_finite(kf, qf[c]), p);
                         const float lb = none ? -INFINITY : l2 + ev;
                         s[mt][2 * hh + c] = l2;
                         sb[mt][2 * hh + c] = lb;

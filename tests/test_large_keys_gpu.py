@@ -3,9 +3,10 @@ drafted path completes, are their means, which are numbers although the keys' su
 import pytest
 import torch
 
+import oracle
 from sparse_hierarchical_attention_pool_b200 import dash_attn as da
 from sparse_hierarchical_attention_pool_b200 import inputs
-from test_cache8_gpu import close, i32, junk_cache
+from test_cache8_gpu import close, filled, i32, junk_cache
 from test_tree_gpu import drafts, expected, run
 
 gpu = pytest.mark.gpu
@@ -71,3 +72,24 @@ def test_paths_that_complete_a_block_of_large_keys(q8, where):
     got, kh, vh = run(q8, q, kd, vd, [parent], k, v, [L], 1.5, junk=False)
     ref = expected(q[0], kd[0], vd[0], parent, kh[0], vh[0], L, 1.5)
     close(got[0].float().cpu(), ref, float(max(vh.float().abs().max(), vd.float().abs().max())), 1.5, 8, where)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_q8_large_keys_beside_large_queries(d):
+    """Keys of 2^110 in a dim that the query lacks, queries of 2^40 in one that the keys lack: every logit is
+    zero, though the key's and the query's scales multiply to no finite number."""
+    B, Hq, Hkv, T = 1, 4, 2, 192
+    g = torch.Generator().manual_seed(29)
+    k, v = torch.randn(B, Hkv, T, d, generator=g), torch.randn(B, Hkv, T, d, generator=g)
+    q = torch.zeros(B, Hq, d)
+    k[..., 7], q[..., 7] = 0.0, 2.0 ** 40
+    for t in (5, 70, 150):
+        k[:, :, t, 3] = 2.0 ** 110
+    k, v, q = k.bfloat16(), v.bfloat16(), q.bfloat16()
+    c = filled(B, Hkv, T, d, k, v)
+    kh, vh = (x.cpu() for x in da.dash_cache_read(*c[:4], T))
+    out, ws = da.dash_decode_q8(q.cuda(), *c, i32([T]), coarse_scale=0.05)
+    assert da.dash_get_device_status(ws) == 0
+    ref, _, _ = oracle.forward_rows(q[0], kh, vh, [(0, h, T - 1) for h in range(Hq)], Hq, 64, 1.5, 0.05)
+    close(out[0].float().cpu(), ref, float(vh.float().abs().max()), 1.5, 11)
