@@ -36,9 +36,8 @@
 //      boxes the eight lanes of a 16-byte load phase then touch all 32 banks, for K and for V.
 #include "cache8.cuh"
 #include "kernels.h"
-#include "mma_sync.cuh"
+#include "mma8.cuh"
 #include "select.cuh"
-#include "sm100.cuh"
 
 namespace dash {
 

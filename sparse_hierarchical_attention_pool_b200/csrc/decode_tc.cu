@@ -33,7 +33,6 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "mma_sync.cuh"
-#include "select.cuh"
 #include "sm100.cuh"
 
 namespace dash {
@@ -59,6 +58,17 @@ struct DtLayout {
     static constexpr uint32_t tab_bytes = kDtTab * kDtMaxG * 4 + kDtTab * 4;   // log-priors, block ids
     static constexpr uint32_t bytes = off_tab + tab_bytes + 1024;
 };
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+// The CTA whose range [U c / n, U (c + 1) / n) holds list position pos.
+__device__ __forceinline__ int dt_cta_of(long long pos, long long U, int n) {
+    return (int)(((pos + 1) * n - 1) / U);
+}
 
 template <int D>
 __global__ void __launch_bounds__(160, 2)

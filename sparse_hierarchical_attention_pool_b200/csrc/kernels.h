@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "serve_geom.cuh"
 
 namespace dash {
 

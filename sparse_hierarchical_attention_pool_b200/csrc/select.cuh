@@ -7,6 +7,12 @@
 
 namespace dash {
 
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" :: "r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// all of the thread's cp.async copies have landed; no access moves across it
+__device__ __forceinline__ void cp_async_done() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
+
 // Shared memory of a decode step's select CTA for the rows it holds at a time (up to 8, one per warp): as many
 // values of each as fit, and the rest from memory in every pass.  It is shared out over the rows there are: one
 // head a group at 262,144 tokens needs 16 KB, not room for 8 rows, and several CTAs fit an SM (40 sequences of 8
@@ -34,8 +40,7 @@ struct WarpRow {
         } else {
             for (int j = lane; j < ns; j += 32) cp_async4(buf + j, row + j);
         }
-        cp_async_commit();
-        cp_async_wait<0>();
+        cp_async_done();
         __syncwarp();
     }
     template <class F>
@@ -479,11 +484,6 @@ static __device__ void decode_plan_tail(const int* count, int* offs, int* plan, 
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
     }
-}
-
-// The CTA whose range [U c / n, U (c + 1) / n) holds list position pos.
-__device__ __forceinline__ int dt_cta_of(long long pos, long long U, int n) {
-    return (int)(((pos + 1) * n - 1) / U);
 }
 
 }  // namespace dash

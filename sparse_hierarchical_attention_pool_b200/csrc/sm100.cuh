@@ -24,10 +24,6 @@ namespace dash {
 // or rejects the arguments (base 16-byte aligned, d * 2 a multiple of 16).
 bool make_tmap_bf16(CUtensorMap* m, const void* ptr, unsigned long long rows, int d, int box_rows);
 
-// The same over a row-major [rows, d] matrix of bytes (d = 64 or 128): boxes of whole rows,
-// swizzled over a row's width (d = 128: 128-byte, d = 64: 64-byte swizzle).
-bool make_tmap_u8(CUtensorMap* m, const void* ptr, unsigned long long rows, int d, int box_rows);
-
 namespace sm100 {
 
 // ------------------------------------------------------------------ mbarriers

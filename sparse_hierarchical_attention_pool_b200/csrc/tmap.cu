@@ -3,6 +3,7 @@
 
 #include <mutex>
 
+#include "mma8.cuh"
 #include "sm100.cuh"
 
 namespace dash {

@@ -133,7 +133,6 @@ tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
             cp_async16(&key_s[row][ch], kd + (size_t)min(row, nodes - 1) * D + ch, row < nodes ? 16 : 0);   // zeros past the nodes
         }
     }
-    cp_async_commit();
     // every node walks up its path (parents come before children, so the walk ends); a parent
     // outside [-1, i) makes the node and its descendants invalid
     __syncthreads();
@@ -151,7 +150,7 @@ tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
     }
     if (tid < g.N && bg % g.Hkv == 0) { w.anc[(size_t)b * g.N + tid] = m; w.depth[(size_t)b * g.N + tid] = dp; }
     if (!__syncthreads_or(may_cross && r + dp >= kBlock)) {
-        cp_async_wait<0>();                                         // the copies land before the CTA's memory is another's
+        cp_async_done();                                            // the copies land before the CTA's memory is another's
         return;
     }
     const int c = tid % TPR * 4, r0 = tid / TPR;
@@ -180,7 +179,7 @@ tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
     const unsigned in_w = __ballot_sync(0xffffffffu, dp >= 0 && r + dp < kBlock);
     if (tid < kMaxNodes && (tid & 31) == 0) in_s[tid >> 5] = in_w;
     *reinterpret_cast<float4*>(&tail_s[r0][c]) = make_float4(t[0], t[1], t[2], t[3]);
-    cp_async_wait<0>();
+    cp_async_done();
     __syncthreads();
     const unsigned long long in = in_s[0] | (unsigned long long)in_s[1] << 32;
     if (tid < kMaxNodes) sum_s[tid] = m & in;
