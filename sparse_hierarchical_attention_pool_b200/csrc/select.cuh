@@ -212,8 +212,9 @@ __device__ __forceinline__ float warp_row_tau(const WarpRow& xr, float m, float 
 }
 
 // Whether a query holds an element that is no finite number (one warp, every lane returns it).  Its row is NaN by
-// its logits; a score of such a row that is infinite, or none that is a number, is no failed solve.
-__device__ __forceinline__ bool row_not_finite(const __nv_bfloat16* q, int d) {
+// its logits; a score of such a row that is infinite, or none that is a number, is no failed solve.  Not inlined:
+// in line, this rare code takes the decode select pass from 64 registers to 104 and a step of 4 x 1M tokens from 242 us to 266.
+static __device__ __noinline__ bool row_not_finite(const __nv_bfloat16* q, int d) {
     bool bad = false;
     for (int c = threadIdx.x & 31; c < d; c += 32) bad |= !(fabsf(__bfloat162float(q[c])) < INFINITY);
     return __any_sync(0xffffffffu, bad);
