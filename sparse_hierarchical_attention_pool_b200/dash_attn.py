@@ -514,7 +514,8 @@ def _refuse(t, dtype, shape, dev, name):
 
 def _ptr(t, dtype, shape, dev, name):
     """Address of a contiguous tensor of this type and shape on device index `dev`."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0 \
+            or not t.is_contiguous():
         _refuse(t, dtype, shape, dev, name)
     return t.data_ptr()
 
@@ -525,8 +526,7 @@ def _opt(t, dtype, shape, dev, name):
 
 def _ksum(ksum, B, Hkv, Tmax, d, block, dev):
     """Block summaries [B, Hkv, Tmax // block, d] (one row at least, as dash_block_summary makes them)."""
-    n = Tmax // block
-    return _ptr(ksum, torch.float32, (B, Hkv, n if n or ksum.shape[2] == 0 else 1, d), dev, "ksum")
+    return _ptr(ksum, torch.float32, (B, Hkv, max(Tmax // block, 1), d), dev, "ksum")
 
 
 def _on(stream, dev):
