@@ -514,10 +514,12 @@ def _refuse(t, dtype, shape, dev, name):
 
 def _ptr(t, dtype, shape, dev, name):
     """Address of a contiguous tensor of this type and shape on device index `dev`."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0 \
-            or not t.is_contiguous():
-        _refuse(t, dtype, shape, dev, name)
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0 and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:                         # no tensor
+        pass
+    _refuse(t, dtype, shape, dev, name)
 
 
 def _opt(t, dtype, shape, dev, name):
@@ -529,11 +531,14 @@ def _ksum(ksum, B, Hkv, Tmax, d, block, dev):
     return _ptr(ksum, torch.float32, (B, Hkv, max(Tmax // block, 1), d), dev, "ksum")
 
 
+_CURRENT = contextlib.nullcontext()
+
+
 def _on(stream, dev):
     """Context in which a call's own tensors are allocated: with a stream given they belong to it, so their
     memory is neither taken from work that is pending on the current stream nor given back to it early."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _CURRENT
     if stream.device.index != dev:
         raise ValueError(f"stream is on device {stream.device.index}, the call's first tensor on {dev}")
     return torch.cuda.stream(stream)
@@ -585,14 +590,15 @@ def dash_cache_append(k_new, v_new, kv_len, k_cache, v_cache, k_scale, v_scale, 
     if n is None:
         n = rows if src is None else src.shape[1]
     dev, full, flat = k_new.get_device(), (B, Hkv, Tmax, d), (B, Hkv, Tmax)
-    args = (_ptr(k_new, torch.bfloat16, k_new.shape, dev, "k_new"), _ptr(v_new, torch.bfloat16, k_new.shape, dev, "v_new"),
-            _opt(src, torch.int32, (B, n), dev, "src"), _opt(n_new, torch.int32, (B,), dev, "n_new"),
-            _ptr(kv_len, torch.int32, (B,), dev, "kv_len"),
-            _ptr(k_cache, _E4M3, full, dev, "k_cache"), _ptr(v_cache, _E4M3, full, dev, "v_cache"),
-            _ptr(k_scale, _U8, flat, dev, "k_scale"), _ptr(v_scale, _U8, flat, dev, "v_scale"),
-            None if ksum is None else _ksum(ksum, B, Hkv, Tmax, d, block, dev))
-    if n != 0:                                     # no tokens: tensors without elements have no address
-        _run("dash_cache_append", dev, stream, *args, B, Hkv, rows, n, Tmax, d, block)
+    # rows without elements have no address, and none is used: the cache's stands for it
+    _run("dash_cache_append", dev, stream,
+         _ptr(k_new, torch.bfloat16, k_new.shape, dev, "k_new") or k_cache.data_ptr(),
+         _ptr(v_new, torch.bfloat16, k_new.shape, dev, "v_new") or k_cache.data_ptr(),
+         _opt(src, torch.int32, (B, n), dev, "src"), _opt(n_new, torch.int32, (B,), dev, "n_new"),
+         _ptr(kv_len, torch.int32, (B,), dev, "kv_len"),
+         _ptr(k_cache, _E4M3, full, dev, "k_cache"), _ptr(v_cache, _E4M3, full, dev, "v_cache"),
+         _ptr(k_scale, _U8, flat, dev, "k_scale"), _ptr(v_scale, _U8, flat, dev, "v_scale"),
+         None if ksum is None else _ksum(ksum, B, Hkv, Tmax, d, block, dev), B, Hkv, rows, n, Tmax, d, block)
 
 
 def dash_cache_read(k_cache, v_cache, k_scale, v_scale, n, start=None, kv_len=None, k_out=None, v_out=None,

@@ -17,7 +17,8 @@ def test_appending_no_tokens():
     none = torch.empty(B, Hkv, 0, d, dtype=torch.bfloat16, device="cuda")
     some = rows(B, Hkv, 3, d, 1).cuda()
     lens, no_src = i32([5, 63]), torch.empty(B, 0, dtype=torch.int32, device="cuda")
-    for x, kw in ((none, {}), (some, {"n": 0}), (some, {"src": no_src}), (none, {"src": no_src}), (some, {"n_new": i32([0, 0])})):
+    for x, kw in ((none, {}), (some, {"n": 0}), (some, {"src": no_src}), (none, {"src": no_src}), (some, {"n_new": i32([0, 0])}),
+                  (none, {"src": i32([[0], [0]])})):                 # no row 0: the sequences are left as they were
         da.dash_cache_append(x, x, lens, *c[:4], ksum=c[4], **kw)
         for a, b in zip(c, before):
             assert same_bits(a, b)
