@@ -393,7 +393,8 @@ DASH_API int dash_decode_noalloc_status(dash_stream_t stream);
  * amax <= 448 * 2^e, and each code is its element * 2^-e rounded to the nearest e4m3 number, ties
  * to even (448 is e4m3's largest: nothing saturates, but for magnitudes above 240 * 2^120, which
  * are held as that, so that every held value is a bf16 number).  A row with a NaN or an infinity gets
- * s = 255 and stands for NaN in every element.
+ * s = 255 and stands for NaN in every element.  So scale bytes are 9 .. 247 or 255 and no code is NaN; the rows that
+ * a step attends, and those that are read, must be like that (zeros, as in a cleared cache, count as zero).
  */
 
 /*
@@ -404,7 +405,9 @@ DASH_API int dash_decode_noalloc_status(dash_stream_t stream);
  *   n_new     device int32 [B] or NULL: tokens appended per sequence, 0 <= n_new[b] <= n; NULL: n
  *   kv_len    device int32 [B]: tokens held before the call (the caller advances it afterwards)
  *   ksum      device fp32 [B, Hkv, Tmax / block, d] or NULL: the summary of every block that the
- *             call completes, the mean of the block's held keys; other entries are left alone
+ *             call completes, the mean of the block's held keys; other entries are left alone.  Learned
+ *             summaries (dash_block_summary_w) are not kept here: pass NULL and make them from
+ *             dash_cache_read's rows
  * A sequence with kv_len[b] < 0, n_new[b] outside [0, n], kv_len[b] + n_new[b] > Tmax or a src
  * entry below n_new[b] outside [0, n_rows) is left as it was.  The summaries depend on what the
  * cache holds alone, so a caller may lower kv_len and append again over rejected tokens.
@@ -433,8 +436,11 @@ DASH_API size_t dash_decode_q8_workspace_size(int B, int Hq, int Hkv, int Tmax, 
  * cache holds, to fp32 rounding of the sums (fewer roundings inside: the weights of the values
  * have 11 significant bits, where dash_decode's have 8).
  *   ksum   as in dash_decode, of the held keys (dash_cache_append keeps it)
- * At most 32 query heads per KV head.  More than 8 are worked on as equal parts of at most 8, each with
- * the union of its own heads' blocks.
+ * Priors are per head (no DASH_HEAD_AGGREGATION).  At most 32 query heads per KV head.  More than 8 are worked on
+ * as equal parts of at most 8, each with the union of its own heads' blocks: 12 heads as 2 parts, but 11, which
+ * nothing divides, as 11 parts that each read their own blocks.
+ * A head whose query holds an element that is no finite number is NaN, the others are not affected, and
+ * dash_get_device_status reports no failed solve for it.
  */
 DASH_API int dash_decode_q8(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
                             const void* v_scale, const float* ksum, const int* kv_len, void* out, int B, int Hq,
@@ -463,8 +469,14 @@ DASH_API size_t dash_decode_tree_workspace_size(int B, int Hq, int Hkv, int N, i
  * Nodes of a sequence with kv_len[b] outside its range, nodes whose parent lies outside
  * [-1, i), and their descendants get zero.  At most 32 query heads per KV head;
  * B * Hkv * Tmax < 2^31.  A drafted key that is no finite number reaches its node and that node's
- * descendants alone; values, and cached keys, that are not finite can reach every row of their
- * sequence and KV group, as they reach every head of a group in dash_decode.
+ * descendants alone (a NaN makes all of them NaN); values, and cached keys, that are not finite can reach every
+ * row of their sequence and KV group, as they reach every head of a group in dash_decode.  A query that is
+ * none makes its own row NaN, and dash_get_device_status reports no failed solve for it.
+ * Roundings: block scores take the summaries to 16 significant bits (as the prefill does; dash_decode takes
+ * all 24), so a block at the border of a row's support may fall on either side; the softmax weights are rounded
+ * to 8 bits for their product with the values, their sum takes them unrounded.
+ * Priors are per head, and a block that a path completes is scored by the mean of its keys: beside learned
+ * summaries in ksum (dash_block_summary_w) that would be another model's score.
  */
 DASH_API int dash_decode_tree(const void* q, const void* k_draft, const void* v_draft, const int* parent,
                               const int* n_nodes, const void* k_cache, const void* v_cache, const float* ksum,

@@ -2,7 +2,7 @@
 //
 // Argument checks happen here, before any launch; kernels live in summary.cu, coarse.cu,
 // coarse_tc.cu, fine_mma.cu, fine_tc.cu, backward.cu, decode.cu, decode_tc.cu, decode_q8.cu,
-// cache8.cu, tree.cu and dump.cu.
+// cache8.cu, tree.cu, tree_tc.cu and dump.cu.
 // Nothing here allocates memory.
 #include <algorithm>
 #include <math.h>

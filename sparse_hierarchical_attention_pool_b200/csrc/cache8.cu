@@ -14,9 +14,10 @@ namespace dash {
 // back when the call completes the block, so the summary is the mean of the values that the
 // cache holds, whatever calls wrote them: it depends on the cache alone and stays right when
 // rows are written again (a drafted path that was not accepted).
-// 4,096 rows of 4 x 8 heads of 128 dims (101 MB) take 23.5 us, 4.3 TB/s.  Instructions and bytes
-// share the time: with 8 elements a lane, whose butterflies and exponents weigh twice as much,
-// and comparisons element by element it took 30.6 us.
+// 4,096 rows of 4 x 8 heads of 128 dims (101 MB) take 23.5 us, 4.3 TB/s.  Neither instructions nor bytes fill
+// it (60 % of the issue slots, 40 % of the DRAM's, most stalls on the loads: a CTA loads, works and stores once,
+// in 2.8 waves); with 8 elements a lane, whose butterflies and exponents weigh twice as much, and comparisons
+// element by element it took 30.6 us.
 template <int D>
 __global__ void __launch_bounds__(256)
 cache_append_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16* __restrict__ v_new,
@@ -36,7 +37,7 @@ cache_append_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int* sb = src ? src + (size_t)b * n : nullptr;
     if (sb) {
-        // a row index outside k_new refuses the sequence
+        // a row index outside k_new refuses the sequence; every CTA looks at the whole list (a path has up to 64 entries)
         int bad = 0;
         for (int i = tid; i < m; i += 256) bad |= (unsigned)sb[i] >= (unsigned)n_rows;
         if (__syncthreads_or(bad)) return;

@@ -239,8 +239,8 @@ tree_scores_kernel(TreeArgs a, TreeWork w, TreeGeom g, float cx) {
 // One warp per row solves its threshold; every selected block sets its bit in the tile's bitmap
 // (a ballot over the lanes is one word).  The CTA that finishes a tile turns the bitmap into
 // the tile's list: selected full blocks ascending, the open block when it holds cached tokens
-// (whether past or own), the tree itself last.  The passes over a row bound it: 4,096 rows of 1,536
-// scores take 14 us and the lists 3.
+// (whether past or own), the tree itself last.  The latency of the passes over a row bounds it (no pipe above a quarter):
+// 4,096 rows of 1,536 scores take 14 us and the lists 3.
 constexpr int kTreeSelWarps = 8;
 
 __global__ void __launch_bounds__(kTreeSelWarps * 32)

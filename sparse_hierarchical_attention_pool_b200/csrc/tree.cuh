@@ -45,7 +45,7 @@ __device__ __forceinline__ bool tree_live(const int* kv_len, const int* n_nodes,
     return *L >= 0 && *L <= g.Tmax && *nodes > 0;
 }
 
-// attention over the tiles' lists on nctas CTAs (at least `per` entries each), and the merge
+// attention over the tiles' lists on at most nctas CTAs, and the merge
 cudaError_t launch_tree_attn(const TreeArgs& a, const TreeWork& w, const TreeGeom& g, float e_pow, float sm2, int nctas,
                              cudaStream_t stream);
 

@@ -26,8 +26,15 @@
 // against 93), eight gain nothing; tiles of f16 codes with the scales outside the product save
 // conversions but need another factor per step in every role, and measured 115.
 //
-// bf16 cache: bound by HBM; 96K, 8 sequences of 32 / 8 heads and 16 nodes: the listed blocks' 1.71 GB in
-// 263 us, 6.5 TB/s.  8-bit cache: bound by the roles' instructions; 32K, 4 sequences, 24 nodes: 45 entries
+// The row sums take the unrounded weights, the products weights of 8 bits (that rounding is what a step's error
+// has beyond its bf16 output's: 0.0022 against 0.0017 in the 2-norm).  Summing the rounded ones, so that a
+// row's add up to one exactly, costs two more instructions a pair in the softmax: 466 us a step against 314 (96K, as
+// below), 112 against 92 (8-bit, 32K).
+//
+// bf16 cache: bound by HBM and the softmax's instructions alike; 96K, 8 sequences of 32 / 8 heads and 16 nodes:
+// the listed blocks' 1.71 GB in 263 us, 6.5 TB/s, at 1965 MHz.  Steps that follow one another draw the card's 1000 W
+// within a second; at the 1550 MHz that its power cap leaves then, a whole step takes 355 us and not 316.
+// 8-bit cache: bound by the roles' instructions; 32K, 4 sequences, 24 nodes: 45 entries
 // a CTA in 55 to 62 us, 2,500 cycles each, of which the converters, which wait for nothing, need all.
 // Every wait is bounded; a CTA that gives up sets a status bit.
 #include "cache8.cuh"
